@@ -83,6 +83,35 @@ _lib.attn_bwd_f32_workspace_bytes.argtypes = [_i, _i, _i, _i]
 _lib.attn_bwd_f32_workspace_bytes.restype = _sz
 _lib.attn_bwd_f32.argtypes = [_fp, _fp, _fp, _fp, _fp, _fp, _fp, _fp, _fp, _i, _i, _i, _i, _f, _vp, _sz, _vp]
 _lib.attn_bwd_f32.restype = _i
+class attn_q8_cache(ctypes.Structure):
+    """Pointers and sizes of an 8-bit block cache (include/attn.h)."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("bounds", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("recent_k", ctypes.c_void_p),
+                ("recent_v", ctypes.c_void_p), ("B", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("blocks", ctypes.c_int32), ("D", ctypes.c_int32)]
+
+
+class attn_q8_decode_options(ctypes.Structure):
+    """Options of attn_q8_decode (include/attn.h): block lists, kept weights."""
+    _fields_ = [("blocks", ctypes.c_void_p), ("blocks_n", ctypes.c_int32), ("weight", ctypes.c_int32)]
+
+
+_qp, _qop = ctypes.POINTER(attn_q8_cache), ctypes.POINTER(attn_q8_decode_options)
+_lib.attn_q8_append.argtypes = [_qp, _vp, _vp, _i, _vp, _vp, _sp, _vp]
+_lib.attn_q8_append.restype = _i
+_lib.attn_q8_read.argtypes = [_qp, _vp, _vp, _i, _vp, _vp, _vp]
+_lib.attn_q8_read.restype = _i
+_lib.attn_q8_decode_workspace_bytes.argtypes = [_qp, _i, _i, _qop]
+_lib.attn_q8_decode_workspace_bytes.restype = _sz
+_lib.attn_q8_decode.argtypes = [_qp, _vp, _vp, _fp, _vp, _i, _i, _f, _sp, _qop, _vp, _sz, _vp]
+_lib.attn_q8_decode.restype = _i
+_lib.attn_q8_select.argtypes = [_qp, _vp, _vp, _vp, _i, _i, _i, _sp, _vp]
+_lib.attn_q8_select.restype = _i
+_lib.attn_q8_evict_workspace_bytes.argtypes = [_qp]
+_lib.attn_q8_evict_workspace_bytes.restype = _sz
+_lib.attn_q8_evict.argtypes = [_qp, _qp, _vp, _vp, _vp, _i, _i, _i, _vp, _sz, _vp]
+_lib.attn_q8_evict.restype = _i
+Q8_BLOCK = 64
 _lib.attn_dropout_mask_bytes.argtypes = [_i, _i, _i]
 _lib.attn_dropout_mask_bytes.restype = _sz
 _lib.attn_device_error.argtypes = [_vp]
@@ -99,7 +128,9 @@ EXPORTED = ("attn_status_string", "attn_version", "attn_last_launch_count", "att
             "attn_bwd_f32", "attn_device_error", "attn_profile_next_call",
             "attn_selftest_wait_timeout", "attn_selftest_device_check", "attn_bwd_noalloc", "attn_fwd_strided",
             "attn_bwd_strided", "attn_fwd_ex", "attn_bwd_ex", "attn_fwd_f32_ex", "attn_bwd_f32_ex",
-            "attn_decode", "attn_dropout_mask_bytes")
+            "attn_decode", "attn_dropout_mask_bytes", "attn_q8_append", "attn_q8_read",
+            "attn_q8_decode_workspace_bytes", "attn_q8_decode", "attn_q8_select",
+            "attn_q8_evict_workspace_bytes", "attn_q8_evict")
 
 
 class AttnError(RuntimeError):
@@ -508,3 +539,231 @@ def attn_decode(q, k, v, o=None, lse=None, scale: Optional[float] = None, stream
         _raise(_lib.attn_decode(*ptrs, B, H, Tq, Tk, D, scale, st, _stream_handle(stream)),
                "attn_decode")
     return o, lse
+
+
+class Q8Cache:
+    """A cache of keys and values in 8 bits, by blocks of 64 tokens (layout and
+    rules: include/attn.h): the tensors, and the structure the library takes.
+    ``bounds`` and ``weight`` may be None (no attn_q8_select; no kept weights
+    and no attn_q8_evict).  The tensors' addresses are taken once: replace a
+    tensor by making another Q8Cache.
+
+    Sequence lengths are the caller's: an int32 CUDA tensor ``lens`` [B] that
+    counts the new tokens before they are appended."""
+    __slots__ = ("k_codes", "v_codes", "scales", "bounds", "weight", "recent_k", "recent_v", "B", "H",
+                 "blocks", "D", "device", "struct", "ref")
+
+    def __init__(self, k_codes, v_codes, scales, bounds, weight, recent_k, recent_v):
+        torch = _torch()
+        if not isinstance(v_codes, torch.Tensor) or v_codes.dim() != 5:
+            raise ValueError("expected v_codes [B, H, blocks, D, 64]")
+        B, H, blocks, D, _ = v_codes.shape
+        S = max(1, min(D, 64))
+        _check(k_codes, "k_codes", torch.uint8, (B, H, blocks, D // S, Q8_BLOCK, S))
+        _check(v_codes, "v_codes", torch.uint8, (B, H, blocks, D, Q8_BLOCK))
+        _check(scales, "scales", torch.float32, (B, H, blocks, 2))
+        if bounds is not None:
+            _check(bounds, "bounds", torch.int8, (B, H, blocks, 2, D))
+        if weight is not None:
+            _check(weight, "weight", torch.float32, (B, H, blocks))
+        _check(recent_k, "recent_k", torch.bfloat16, (B, H, 2 * Q8_BLOCK, D))
+        _check(recent_v, "recent_v", torch.bfloat16, (B, H, 2 * Q8_BLOCK, D))
+        self.k_codes, self.v_codes, self.scales = k_codes, v_codes, scales
+        self.bounds, self.weight, self.recent_k, self.recent_v = bounds, weight, recent_k, recent_v
+        self.B, self.H, self.blocks, self.D, self.device = B, H, blocks, D, v_codes.device
+        parts = (k_codes, v_codes, scales, bounds, weight, recent_k, recent_v)
+        if any(t is not None and t.device != self.device for t in parts):
+            raise ValueError("the cache's tensors must be on one device")
+        self.struct = attn_q8_cache(*(None if t is None else t.data_ptr() for t in parts), B, H, blocks, D)
+        self.ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def empty(cls, B: int, H: int, D: int, max_tokens: int, device="cuda", bounds: bool = True,
+              weight: bool = True) -> "Q8Cache":
+        """A cache of zeros for B sequences of up to max_tokens tokens, H key heads of size D."""
+        torch = _torch()
+        nb, S = max(1, -(-int(max_tokens) // Q8_BLOCK)), max(1, min(D, 64))
+        new = lambda dtype, *shape: torch.zeros(B, H, *shape, dtype=dtype, device=device)
+        return cls(new(torch.uint8, nb, D // S, Q8_BLOCK, S), new(torch.uint8, nb, D, Q8_BLOCK),
+                   new(torch.float32, nb, 2), new(torch.int8, nb, 2, D) if bounds else None,
+                   new(torch.float32, nb) if weight else None,
+                   new(torch.bfloat16, 2 * Q8_BLOCK, D), new(torch.bfloat16, 2 * Q8_BLOCK, D))
+
+
+def _check_cache(cache, name="cache"):
+    if type(cache) is not Q8Cache:
+        raise TypeError(f"{name} must be a Q8Cache")
+    return cache.device
+
+
+def _check_on(t, name, device):
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _used_on(stream, device, *tensors):
+    """Tells the allocator that tensors made for this call are in use on a
+    stream other than the current one."""
+    if stream is not None and stream != _torch().cuda.current_stream(device):
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def attn_q8_append(cache, k, v, lens, new_lens=None, stream=None) -> None:
+    """Takes the newest tokens' keys and values (bf16 [B, H, n, D], contiguous
+    or strided views) into the cache.  ``lens`` [B] int32 counts them already;
+    ``new_lens`` [B] int32: how many of the n rows are sequence b's (the first
+    ones; None: all n)."""
+    torch = _torch()
+    device = _check_cache(cache)
+    B, H, n, D = _shape4(k)
+    shape = (cache.B, cache.H, n, cache.D)
+    kp, vp = _check_view(k, "k", shape), _check_view(v, "v", shape)
+    lp = _check(lens, "lens", torch.int32, (cache.B,))
+    np_ = None if new_lens is None else _check(new_lens, "new_lens", torch.int32, (cache.B,))
+    for t, name in ((k, "k"), (v, "v"), (lens, "lens"), (new_lens, "new_lens")):
+        if t is not None:
+            _check_on(t, name, device)
+    st = None if k.is_contiguous() and v.is_contiguous() else _strides_of(k, v)
+    with _device(device):
+        _raise(_lib.attn_q8_append(cache.ref, kp, vp, n, lp, np_, st, _stream_handle(stream)), "attn_q8_append")
+
+
+def attn_q8_read(cache, lens, n: int, starts=None, k=None, v=None, stream=None):
+    """Positions starts[b] .. + n - 1 (None: from 0) as the cache holds them,
+    in bf16 [B, H, n, D], zero past a sequence's end.  Returns (k, v)."""
+    torch = _torch()
+    device = _check_cache(cache)
+    shape = (cache.B, cache.H, int(n), cache.D)
+    new = [t is None for t in (k, v)]
+    k = torch.empty(shape, dtype=torch.bfloat16, device=device) if new[0] else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=device) if new[1] else v
+    lp = _check(lens, "lens", torch.int32, (cache.B,))
+    sp = None if starts is None else _check(starts, "starts", torch.int32, (cache.B,))
+    kp, vp = _check(k, "k", torch.bfloat16, shape), _check(v, "v", torch.bfloat16, shape)
+    for t, name in ((k, "k"), (v, "v"), (lens, "lens"), (starts, "starts")):
+        if t is not None:
+            _check_on(t, name, device)
+    with _device(device):
+        _raise(_lib.attn_q8_read(cache.ref, lp, sp, int(n), kp, vp, _stream_handle(stream)), "attn_q8_read")
+        _used_on(stream, device, *(t for t, made in zip((k, v), new) if made))
+    return k, v
+
+
+_Q8_WEIGHT = {None: 0, "set": 1, "add": 2}
+
+
+def attn_q8_decode_workspace_bytes(cache, H: int, Tq: int, blocks_n: int = 0, weight: Optional[str] = None) -> int:
+    opts = attn_q8_decode_options(None, blocks_n, _Q8_WEIGHT[weight])
+    return int(_lib.attn_q8_decode_workspace_bytes(cache.ref, H, Tq, ctypes.byref(opts)))
+
+
+def attn_q8_decode(q, cache, lens, o=None, lse=None, scale: Optional[float] = None, blocks=None,
+                   weight: Optional[str] = None, workspace=None, stream=None):
+    """Attention of the newest Tq tokens' queries (bf16 [B, Hq, Tq, D], Hq a
+    multiple of the cache's heads) over the cache, which holds those tokens
+    too.  ``blocks``: int32 [B, H, Tq, n] from attn_q8_select, the closed
+    blocks to attend to (the open one always is).  ``weight``: "set" or "add"
+    to keep the attention weight of each closed block in cache.weight.
+    Returns (O [B, Hq, Tq, D], lse [B, Hq, Tq])."""
+    torch = _torch()
+    device = _check_cache(cache)
+    B, H, Tq, D = _shape4(q)
+    if weight not in _Q8_WEIGHT:
+        raise ValueError("weight must be None, 'set' or 'add'")
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    shape = (cache.B, H, Tq, cache.D)
+    made = []
+    if o is None:
+        made.append(o := torch.empty(shape, dtype=torch.bfloat16, device=device))
+    if lse is None:
+        made.append(lse := torch.empty((cache.B, H, Tq), dtype=torch.float32, device=device))
+    qp, op = _check_view(q, "q", shape), _check_view(o, "o", shape)
+    ep = _check(lse, "lse", torch.float32, (cache.B, H, Tq))
+    lp = _check(lens, "lens", torch.int32, (cache.B,))
+    n, bp = 0, None
+    if blocks is not None:
+        if not isinstance(blocks, torch.Tensor) or blocks.dim() != 4 or blocks.shape[3] < 1:
+            raise ValueError("blocks must be a [B, H, Tq, n] tensor")
+        n = blocks.shape[3]
+        bp = _check(blocks, "blocks", torch.int32, (cache.B, cache.H, Tq, n))
+        _check_on(blocks, "blocks", device)
+    for t, name in ((q, "q"), (o, "o"), (lse, "lse"), (lens, "lens")):
+        _check_on(t, name, device)
+    opts = ctypes.byref(attn_q8_decode_options(bp, n, _Q8_WEIGHT[weight]))
+    if workspace is None:
+        need = _lib.attn_q8_decode_workspace_bytes(cache.ref, H, Tq, opts)
+        made.append(workspace := torch.empty(max(need, 1), dtype=torch.uint8, device=device))
+    elif not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    st = None if q.is_contiguous() and o.is_contiguous() else _strides_of(q, o)
+    with _device(device):
+        _raise(_lib.attn_q8_decode(cache.ref, qp, op, ep, lp, H, Tq, scale, st, opts, workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _stream_handle(stream)),
+               "attn_q8_decode")
+        _used_on(stream, device, *made)
+    return o, lse
+
+
+def attn_q8_select(q, cache, lens, n: int, blocks=None, stream=None):
+    """The n closed blocks that each query of q (as in attn_q8_decode) is
+    likely to attend to most, by a bound on their keys' products with it:
+    int32 [B, H, Tq, n], ascending, -1 behind the last."""
+    torch = _torch()
+    device = _check_cache(cache)
+    B, Hq, Tq, D = _shape4(q)
+    shape = (cache.B, cache.H, Tq, int(n))
+    new = blocks is None
+    blocks = torch.empty(shape, dtype=torch.int32, device=device) if new else blocks
+    qp = _check_view(q, "q", (cache.B, Hq, Tq, cache.D))
+    lp = _check(lens, "lens", torch.int32, (cache.B,))
+    bp = _check(blocks, "blocks", torch.int32, shape)
+    for t, name in ((q, "q"), (lens, "lens"), (blocks, "blocks")):
+        _check_on(t, name, device)
+    st = None if q.is_contiguous() else _strides_of(q)
+    with _device(device):
+        _raise(_lib.attn_q8_select(cache.ref, qp, lp, bp, int(n), Hq, Tq, st, _stream_handle(stream)),
+               "attn_q8_select")
+        if new:
+            _used_on(stream, device, blocks)
+    return blocks
+
+
+def attn_q8_evict_workspace_bytes(cache) -> int:
+    return int(_lib.attn_q8_evict_workspace_bytes(cache.ref))
+
+
+def attn_q8_evict(cache, lens, keep: int, sink: int = 0, recent: int = 1, out=None, lens_out=None, kept=None,
+                  workspace=None, stream=None):
+    """Keeps `keep` closed blocks of each sequence and head: the first `sink`,
+    the last `recent` and those with the largest cache.weight between them,
+    moved to the front of ``out`` (None: of the cache itself).  Returns
+    (lens_out [B], kept [B, H, keep]: the places the blocks came from, -1
+    behind the last)."""
+    torch = _torch()
+    device = _check_cache(cache)
+    out = cache if out is None else out
+    _check_cache(out, "out")
+    if out.device != device:
+        raise ValueError(f"out must be on {device}, got {out.device}")
+    made = []
+    if lens_out is None:
+        made.append(lens_out := torch.empty(cache.B, dtype=torch.int32, device=device))
+    if kept is None:
+        made.append(kept := torch.empty((cache.B, cache.H, max(int(keep), 0)), dtype=torch.int32, device=device))
+    lp = _check(lens, "lens", torch.int32, (cache.B,))
+    op = _check(lens_out, "lens_out", torch.int32, (cache.B,))
+    kp = _check(kept, "kept", torch.int32, (cache.B, cache.H, int(keep)))
+    if workspace is None:
+        made.append(workspace := torch.empty(_lib.attn_q8_evict_workspace_bytes(cache.ref), dtype=torch.uint8,
+                                             device=device))
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    for t, name in ((lens, "lens"), (lens_out, "lens_out"), (kept, "kept"), (workspace, "workspace")):
+        _check_on(t, name, device)
+    with _device(device):
+        _raise(_lib.attn_q8_evict(cache.ref, out.ref, lp, op, kp, int(keep), int(sink), int(recent),
+                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                  _stream_handle(stream)), "attn_q8_evict")
+        _used_on(stream, device, *made)
+    return lens_out, kept

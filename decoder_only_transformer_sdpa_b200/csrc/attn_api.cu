@@ -24,6 +24,8 @@ int g_cc_major[kMaxDevices];  // 0 = not yet queried
 thread_local int t_last_launches = 0;
 thread_local cudaEvent_t t_prof_start = nullptr, t_prof_end = nullptr;
 
+}  // namespace
+
 // Takes the armed profiling events (if any) for the call being made.
 LaunchInfo take_launch_info() {
     LaunchInfo li;
@@ -33,11 +35,14 @@ LaunchInfo take_launch_info() {
     return li;
 }
 
+namespace {
 int current_device(int &dev) {
     if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
     if (dev < 0 || dev >= kMaxDevices) return ATTN_ERR_DEVICE;
     return ATTN_OK;
 }
+
+}  // namespace
 
 // Checks the current device is sm_100 and returns its error-word address.
 int device_setup(int **err_addr) {
@@ -64,6 +69,17 @@ int device_setup(int **err_addr) {
     return ATTN_OK;
 }
 
+int finish(cudaError_t e, const LaunchInfo &li) {
+    if (e != cudaSuccess) {
+        cudaGetLastError();  // clear a sticky launch error of this call
+        return ATTN_ERR_CUDA;
+    }
+    t_last_launches = li.kernels;
+    return ATTN_OK;
+}
+
+namespace {
+
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 int check_shape(int B, int H, int T, int D, int dmax) {
@@ -80,15 +96,6 @@ int check_scale(float scale) {
 }
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-int finish(cudaError_t e, const LaunchInfo &li) {
-    if (e != cudaSuccess) {
-        cudaGetLastError();  // clear a sticky launch error of this call
-        return ATTN_ERR_CUDA;
-    }
-    t_last_launches = li.kernels;
-    return ATTN_OK;
-}
 
 bool bf16_d_supported(int D) { return D == 32 || D == 64 || D == 128; }
 bool decode_d_supported(int D) { return D == 32 || D == 64; }
@@ -112,6 +119,7 @@ ATTN_API const char *attn_status_string(int status) {
         case ATTN_ERR_SCALE: return "scale must be finite and positive";
         case ATTN_ERR_OPTION: return "unsupported attn_options value";
         case ATTN_ERR_DEVICE_CHECK: return "a device-side bounds check failed (debug build)";
+        case ATTN_ERR_LENGTH: return "a sequence length or block list on the device is out of range";
         default: return "unknown status";
     }
 }
@@ -465,6 +473,7 @@ ATTN_API int attn_device_error(cudaStream_t stream) {
         if (cudaMemcpy(err, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
             return ATTN_ERR_CUDA;
         if (h == kErrBounds) return ATTN_ERR_DEVICE_CHECK;
+        if (h == kErrLength) return ATTN_ERR_LENGTH;
         return h == kErrLayout ? ATTN_ERR_CUDA : ATTN_ERR_TIMEOUT;
     }
     return ATTN_OK;

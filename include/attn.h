@@ -74,8 +74,10 @@ typedef enum {
     ATTN_ERR_DEVICE = -8,        /* current device is not sm_100 (B200 class)       */
     ATTN_ERR_SCALE = -9,         /* scale is not finite and positive                */
     ATTN_ERR_OPTION = -10,       /* an attn_options field holds an unsupported value */
-    ATTN_ERR_DEVICE_CHECK = -11  /* a device-side bounds check failed (the debug
+    ATTN_ERR_DEVICE_CHECK = -11, /* a device-side bounds check failed (the debug
                                     build, libattn_debug.so, only)               */
+    ATTN_ERR_LENGTH = -12        /* a sequence length or block list held on the
+                                    device is out of range                       */
 } attn_status;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -266,6 +268,155 @@ int attn_decode(const void *q, const void *k, const void *v, void *o, float *lse
                 int B, int H, int Tq, int Tk, int D, float scale, const attn_strides *strides,
                 cudaStream_t stream);
 
+/* ---------------- a cache of keys and values in 8 bits ------------------ */
+
+/* Decode reads every kept key and value once per new token, so its time and
+ * the memory that a batch of texts needs are the cache's bytes.  This cache
+ * holds them in 8 bits, by blocks of 64 tokens with one scale for the keys and
+ * one for the values of a block and head, and lets attention read less than
+ * all of it (attn_q8_select) or bounds its length (attn_q8_evict).  (The pages
+ * keep no cache at all: "nanoGPT — 架构与原理", section 5 "边界与局限".)
+ *
+ * Contents.  A block is quantised once, when its 64 tokens are there (it is
+ * then "closed"); the tokens behind the last closed block (the "open block")
+ * are held exactly.  With most = max |x| over a closed block's 64 x D numbers
+ * (keys and values apart):
+ *
+ *   scale = most / 127, code = 128 + rint(127 x / most) (halves to even),
+ *   x is held as (code - 128) * scale: off by at most most / 254.
+ *
+ * A block with an infinity or a NaN gets a NaN scale (all of it reads as NaN).
+ *
+ * Lengths.  lens [B] (int32, on the device) holds each sequence's number of
+ * tokens and belongs to the caller, who adds the new tokens to it before an
+ * append; 0 <= lens[b] <= 64 * blocks + 63.  Being on the device, it may change
+ * between replays of a captured graph.  A length out of range is treated as 0
+ * (an append or eviction leaves the sequence as it is) and makes
+ * attn_device_error() return ATTN_ERR_LENGTH, as does a bad new_lens, starts
+ * or block list.
+ *
+ * recent_k, recent_v hold the newest positions in bf16, position p in row
+ * p % 128: all of the open block and of the closed block before it.  So an
+ * append of up to 64 tokens may be repeated, and tokens may be taken back
+ * (drafted ones that were refused): lens may fall again as far as the start of
+ * the last closed block.
+ *
+ * The caller owns all of the memory (device; zeros at the start do).  Calls on
+ * one cache are ordered by their stream; calls on different streams are the
+ * caller's to order.
+ *
+ *   k_codes  uint8 [B, H, blocks, D / S, 64, S], S = min(D, 64), 16-byte aligned
+ *   v_codes  uint8 [B, H, blocks, D, 64], 16-byte aligned
+ *   scales   float [B, H, blocks, 2] (keys, values), 8-byte aligned
+ *   bounds   int8 [B, H, blocks, 2, D]: the smallest and the largest code - 128
+ *            of each key channel, 16-byte aligned; NULL: not kept (then there
+ *            is no attn_q8_select)
+ *   weight   float [B, H, blocks]: attention weight each closed block has
+ *            received, set to 0 when it closes; NULL: not kept (then there is
+ *            no ATTN_Q8_WEIGHT_* and no attn_q8_evict)
+ *   recent_k, recent_v  bf16 [B, H, 128, D], 16-byte aligned
+ *
+ * B sequences, H key heads, blocks <= 32768 closed blocks a sequence, D 32, 64
+ * or 128 (all three bf16 head sizes of the forward). */
+#define ATTN_Q8_BLOCK 64
+typedef struct {
+    void *k_codes, *v_codes;
+    float *scales;
+    void *bounds;
+    float *weight;
+    void *recent_k, *recent_v;
+    int32_t B, H, blocks, D;
+} attn_q8_cache;
+
+/* Takes in new tokens: k, v bf16 [B, H, n, D] (strides: NULL for contiguous
+ * tensors, else strides[0..1] for k, v under the rules of attn_fwd_strided).
+ * Rows 0 .. m - 1 of sequence b become its newest m tokens, positions
+ * lens[b] - m .. lens[b] - 1, with m = new_lens[b] (int32 [B] on the device,
+ * 0 <= m <= n and m <= lens[b]) or n when new_lens is NULL: a padded batch of
+ * prompts is left-aligned with new_lens = lens, and a sequence with m = 0 is
+ * left alone.  One launch, no workspace. */
+int attn_q8_append(const attn_q8_cache *cache, const void *k, const void *v, int n,
+                   const int32_t *lens, const int32_t *new_lens, const attn_strides *strides,
+                   cudaStream_t stream);
+
+/* Reads positions starts[b] .. starts[b] + n - 1 (starts: int32 [B] on the
+ * device, NULL: from 0) as they are held, rounded to bf16, into k, v [B, H, n,
+ * D] contiguous; rows of positions past the sequence's end are zero.  E.g. to
+ * hand a text over to attn_fwd, or to store it. */
+int attn_q8_read(const attn_q8_cache *cache, const int32_t *lens, const int32_t *starts, int n,
+                 void *k, void *v, cudaStream_t stream);
+
+/* Options of attn_q8_decode (NULL: every block, weights not kept).
+ *
+ * blocks, blocks_n: int32 [B, cache H, Tq, blocks_n] on the device, as
+ *   attn_q8_select writes it: for each key head and query the closed blocks to
+ *   attend to, ascending, -1 behind the last.  The open block is always
+ *   attended to.  Entries out of order or not closed are skipped
+ *   (ATTN_ERR_LENGTH from attn_device_error()).  NULL and 0: every block.
+ * weight: ATTN_Q8_WEIGHT_SET or _ADD: cache->weight of each closed block
+ *   becomes (or grows by) the attention weight that this call's queries gave
+ *   its tokens, summed over the queries and the heads that share the key
+ *   head.  Not together with blocks (ATTN_ERR_OPTION). */
+enum { ATTN_Q8_WEIGHT_NONE = 0, ATTN_Q8_WEIGHT_SET = 1, ATTN_Q8_WEIGHT_ADD = 2 };
+typedef struct {
+    const int32_t *blocks;
+    int32_t blocks_n;
+    int32_t weight;
+} attn_q8_decode_options;
+
+/* Bytes of device workspace attn_q8_decode needs for a cache of these sizes
+ * (its pointers are not looked at) and these options; 0 on a bad shape. */
+size_t attn_q8_decode_workspace_bytes(const attn_q8_cache *cache, int H, int Tq,
+                                      const attn_q8_decode_options *opts);
+
+/* Attention of the Tq newest tokens of each sequence, appended before: as
+ * attn_decode, with keys and values from the cache and a length of its own for
+ * each sequence.  q, o: bf16 [B, H, Tq, D] (strides: NULL, or strides[0..1] for
+ * q, o), lse: float32 [B, H, Tq] contiguous.  H query heads, a multiple of the
+ * cache's (query head h reads key head h / (H / cache H); at most 64 share
+ * one).  1 <= Tq <= ATTN_DECODE_MAX_QUERIES.  Query r is the token at position
+ * lens[b] - Tq + r; where that is below zero nothing is seen: o = 0, lse =
+ * -inf.  workspace: at least attn_q8_decode_workspace_bytes bytes, 256-byte
+ * aligned, its contents do not matter.  Two launches, a third one with
+ * weights. */
+int attn_q8_decode(const attn_q8_cache *cache, const void *q, void *o, float *lse,
+                   const int32_t *lens, int H, int Tq, float scale, const attn_strides *strides,
+                   const attn_q8_decode_options *opts, void *workspace, size_t workspace_bytes,
+                   cudaStream_t stream);
+
+/* Chooses the n closed blocks that each query is likely to attend to most, for
+ * attn_q8_decode's options: blocks int32 [B, cache H, Tq, n], ascending, -1
+ * where a query has fewer than n (only blocks that begin at or before its own
+ * position count).  The score bounds a block's products with the query, the
+ * query in 8 bits too:
+ *
+ *   c = rint(127 q / max|q|), dot_j = sum_d max(c_d lo_jd, c_d hi_jd),
+ *   score_j = (dot_j * kscale_j) * (max|q| / 127), each product in float32,
+ *
+ * and the largest over the query heads that share the key head.  Ties go to
+ * the lowest index, NaN ranks first.  q as attn_q8_decode (strides: NULL, or
+ * q's).  One launch, no workspace. */
+int attn_q8_select(const attn_q8_cache *cache, const void *q, const int32_t *lens, int32_t *blocks,
+                   int n, int H, int Tq, const attn_strides *strides, cudaStream_t stream);
+
+/* Bytes of device workspace attn_q8_evict needs; 0 on a bad shape. */
+size_t attn_q8_evict_workspace_bytes(const attn_q8_cache *cache);
+
+/* Drops closed blocks until each sequence and head has at most `keep` (>= 1) of
+ * them: the first `sink` and the last `recent` ones stay, and of the others
+ * those with the largest cache->weight (ties to the lowest index; sink +
+ * recent <= keep).  The kept blocks move to the front in order, with scales,
+ * bounds and weight, of `out`: the same cache (the same pointers), or another
+ * one that shares no memory with it and holds at least min(keep, blocks)
+ * blocks.  lens_out [B] (may be lens) gets the new lengths: min(closed, keep)
+ * * 64 + lens[b] % 64; kept int32 [B, H, keep] the places the blocks came from,
+ * ascending, -1 behind the last.  Heads keep different blocks, all of them
+ * equally many.  workspace: as attn_q8_evict_workspace_bytes, 256-byte
+ * aligned.  Two launches. */
+int attn_q8_evict(const attn_q8_cache *cache, const attn_q8_cache *out, const int32_t *lens,
+                  int32_t *lens_out, int32_t *kept, int keep, int sink, int recent, void *workspace,
+                  size_t workspace_bytes, cudaStream_t stream);
+
 /* ---------------- float32 path: CUDA cores, IEEE expf -------------------- */
 
 /* Forward in float32 (all tensors float32).  1 <= D <= 128. */
@@ -295,7 +446,8 @@ int attn_bwd_f32_ex(const float *q, const float *k, const float *v, const float 
 
 /* Synchronises `stream`, then reads and clears the current device's
  * in-kernel error flag.  Returns ATTN_OK, ATTN_ERR_TIMEOUT (a bounded wait
- * ran out since the last call), ATTN_ERR_DEVICE_CHECK (the debug build
+ * ran out since the last call), ATTN_ERR_LENGTH (a length or block list of an
+ * 8-bit cache's call was out of range), ATTN_ERR_DEVICE_CHECK (the debug build
  * libattn_debug.so only: a kernel's bounds check on a tile coordinate, TMEM
  * column or shared-memory offset failed; the kernel records it and carries
  * on) or ATTN_ERR_CUDA (the sync itself failed, or a kernel found its dynamic
