@@ -551,7 +551,7 @@ class Q8Cache:
     Sequence lengths are the caller's: an int32 CUDA tensor ``lens`` [B] that
     counts the new tokens before they are appended."""
     __slots__ = ("k_codes", "v_codes", "scales", "bounds", "weight", "recent_k", "recent_v", "B", "H",
-                 "blocks", "D", "device", "struct", "ref")
+                 "blocks", "D", "device", "index", "struct", "ref", "needs")
 
     def __init__(self, k_codes, v_codes, scales, bounds, weight, recent_k, recent_v):
         torch = _torch()
@@ -576,6 +576,8 @@ class Q8Cache:
             raise ValueError("the cache's tensors must be on one device")
         self.struct = attn_q8_cache(*(None if t is None else t.data_ptr() for t in parts), B, H, blocks, D)
         self.ref = ctypes.byref(self.struct)
+        self.index = self.device.index
+        self.needs = {}  # workspace bytes by (query heads, new tokens, list length, weights)
 
     @classmethod
     def empty(cls, B: int, H: int, D: int, max_tokens: int, device="cuda", bounds: bool = True,
@@ -593,20 +595,59 @@ class Q8Cache:
 def _check_cache(cache, name="cache"):
     if type(cache) is not Q8Cache:
         raise TypeError(f"{name} must be a Q8Cache")
-    return cache.device
+    return cache.index
 
 
-def _check_on(t, name, device):
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+def _refuse_other_device(t, name, index):
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
 
 
-def _used_on(stream, device, *tensors):
+def _whole(t, name, dtype, shape, index):
+    """The address of a contiguous tensor of this type and shape on device
+    `index`: one test on the common path, the specific error otherwise."""
+    try:
+        if t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    p = _check(t, name, dtype, shape)
+    _refuse_other_device(t, name, index)
+    return p
+
+
+def _view(t, name, shape, index):
+    """The same for a bf16 [B, H, T, D] view with unit stride along D."""
+    try:
+        if (t.get_device() == index and t.dtype is _torch().bfloat16 and t.shape == shape
+                and t.stride(3) == 1):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    p = _check_view(t, name, shape)
+    _refuse_other_device(t, name, index)
+    return p
+
+
+def _used_on(stream, index, *tensors):
     """Tells the allocator that tensors made for this call are in use on a
     stream other than the current one."""
-    if stream is not None and stream != _torch().cuda.current_stream(device):
+    if stream is not None and stream != _torch().cuda.current_stream(index):
         for t in tensors:
             t.record_stream(stream)
+
+
+def _call(fn, where, index, stream, *args):
+    """The library call on device `index`, on `stream` (None: the current one of that device)."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None and torch.cuda.current_device() == index:
+        status = fn(*args, raw(index) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _stream_handle(stream))
+    if status != 0:
+        raise AttnError(status, where)
 
 
 def attn_q8_append(cache, k, v, lens, new_lens=None, stream=None) -> None:
@@ -614,39 +655,33 @@ def attn_q8_append(cache, k, v, lens, new_lens=None, stream=None) -> None:
     or strided views) into the cache.  ``lens`` [B] int32 counts them already;
     ``new_lens`` [B] int32: how many of the n rows are sequence b's (the first
     ones; None: all n)."""
-    torch = _torch()
-    device = _check_cache(cache)
-    B, H, n, D = _shape4(k)
+    i32 = _torch().int32
+    index = _check_cache(cache)
+    n = _shape4(k)[2]
     shape = (cache.B, cache.H, n, cache.D)
-    kp, vp = _check_view(k, "k", shape), _check_view(v, "v", shape)
-    lp = _check(lens, "lens", torch.int32, (cache.B,))
-    np_ = None if new_lens is None else _check(new_lens, "new_lens", torch.int32, (cache.B,))
-    for t, name in ((k, "k"), (v, "v"), (lens, "lens"), (new_lens, "new_lens")):
-        if t is not None:
-            _check_on(t, name, device)
+    kp, vp = _view(k, "k", shape, index), _view(v, "v", shape, index)
+    lp = _whole(lens, "lens", i32, (cache.B,), index)
+    np_ = None if new_lens is None else _whole(new_lens, "new_lens", i32, (cache.B,), index)
     st = None if k.is_contiguous() and v.is_contiguous() else _strides_of(k, v)
-    with _device(device):
-        _raise(_lib.attn_q8_append(cache.ref, kp, vp, n, lp, np_, st, _stream_handle(stream)), "attn_q8_append")
+    _call(_lib.attn_q8_append, "attn_q8_append", index, stream, cache.ref, kp, vp, n, lp, np_, st)
 
 
 def attn_q8_read(cache, lens, n: int, starts=None, k=None, v=None, stream=None):
     """Positions starts[b] .. + n - 1 (None: from 0) as the cache holds them,
     in bf16 [B, H, n, D], zero past a sequence's end.  Returns (k, v)."""
     torch = _torch()
-    device = _check_cache(cache)
+    index = _check_cache(cache)
     shape = (cache.B, cache.H, int(n), cache.D)
-    new = [t is None for t in (k, v)]
-    k = torch.empty(shape, dtype=torch.bfloat16, device=device) if new[0] else k
-    v = torch.empty(shape, dtype=torch.bfloat16, device=device) if new[1] else v
-    lp = _check(lens, "lens", torch.int32, (cache.B,))
-    sp = None if starts is None else _check(starts, "starts", torch.int32, (cache.B,))
-    kp, vp = _check(k, "k", torch.bfloat16, shape), _check(v, "v", torch.bfloat16, shape)
-    for t, name in ((k, "k"), (v, "v"), (lens, "lens"), (starts, "starts")):
-        if t is not None:
-            _check_on(t, name, device)
-    with _device(device):
-        _raise(_lib.attn_q8_read(cache.ref, lp, sp, int(n), kp, vp, _stream_handle(stream)), "attn_q8_read")
-        _used_on(stream, device, *(t for t, made in zip((k, v), new) if made))
+    made = []
+    if k is None:
+        made.append(k := cache.recent_k.new_empty(shape))
+    if v is None:
+        made.append(v := cache.recent_k.new_empty(shape))
+    lp = _whole(lens, "lens", torch.int32, (cache.B,), index)
+    sp = None if starts is None else _whole(starts, "starts", torch.int32, (cache.B,), index)
+    kp, vp = (_whole(t, name, torch.bfloat16, shape, index) for t, name in ((k, "k"), (v, "v")))
+    _call(_lib.attn_q8_read, "attn_q8_read", index, stream, cache.ref, lp, sp, int(n), kp, vp)
+    _used_on(stream, index, *made)
     return k, v
 
 
@@ -667,41 +702,44 @@ def attn_q8_decode(q, cache, lens, o=None, lse=None, scale: Optional[float] = No
     to keep the attention weight of each closed block in cache.weight.
     Returns (O [B, Hq, Tq, D], lse [B, Hq, Tq])."""
     torch = _torch()
-    device = _check_cache(cache)
-    B, H, Tq, D = _shape4(q)
-    if weight not in _Q8_WEIGHT:
+    index = _check_cache(cache)
+    _, H, Tq, D = _shape4(q)
+    keep = _Q8_WEIGHT.get(weight)
+    if keep is None:
         raise ValueError("weight must be None, 'set' or 'add'")
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     shape = (cache.B, H, Tq, cache.D)
+    qp = _view(q, "q", shape, index)
+    plain = q.is_contiguous()
     made = []
     if o is None:
-        made.append(o := torch.empty(shape, dtype=torch.bfloat16, device=device))
+        made.append(o := torch.empty_like(q) if plain else q.new_empty(shape))
     if lse is None:
-        made.append(lse := torch.empty((cache.B, H, Tq), dtype=torch.float32, device=device))
-    qp, op = _check_view(q, "q", shape), _check_view(o, "o", shape)
-    ep = _check(lse, "lse", torch.float32, (cache.B, H, Tq))
-    lp = _check(lens, "lens", torch.int32, (cache.B,))
-    n, bp = 0, None
+        made.append(lse := q.new_empty(shape[:3], dtype=torch.float32))
+    op = _view(o, "o", shape, index)
+    ep = _whole(lse, "lse", torch.float32, shape[:3], index)
+    lp = _whole(lens, "lens", torch.int32, (cache.B,), index)
+    n, opts = 0, None
     if blocks is not None:
         if not isinstance(blocks, torch.Tensor) or blocks.dim() != 4 or blocks.shape[3] < 1:
             raise ValueError("blocks must be a [B, H, Tq, n] tensor")
         n = blocks.shape[3]
-        bp = _check(blocks, "blocks", torch.int32, (cache.B, cache.H, Tq, n))
-        _check_on(blocks, "blocks", device)
-    for t, name in ((q, "q"), (o, "o"), (lse, "lse"), (lens, "lens")):
-        _check_on(t, name, device)
-    opts = ctypes.byref(attn_q8_decode_options(bp, n, _Q8_WEIGHT[weight]))
+        opts = attn_q8_decode_options(_whole(blocks, "blocks", torch.int32, (cache.B, cache.H, Tq, n), index), n, keep)
+    elif keep:
+        opts = attn_q8_decode_options(None, 0, keep)
     if workspace is None:
-        need = _lib.attn_q8_decode_workspace_bytes(cache.ref, H, Tq, opts)
-        made.append(workspace := torch.empty(max(need, 1), dtype=torch.uint8, device=device))
-    elif not workspace.is_contiguous() or workspace.device != device:
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    st = None if q.is_contiguous() and o.is_contiguous() else _strides_of(q, o)
-    with _device(device):
-        _raise(_lib.attn_q8_decode(cache.ref, qp, op, ep, lp, H, Tq, scale, st, opts, workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), _stream_handle(stream)),
-               "attn_q8_decode")
-        _used_on(stream, device, *made)
+        need = cache.needs.get((H, Tq, n, keep))
+        if need is None:
+            need = int(_lib.attn_q8_decode_workspace_bytes(cache.ref, H, Tq, opts))
+            cache.needs[(H, Tq, n, keep)] = need
+        if need:
+            made.append(workspace := cache.k_codes.new_empty(need))
+    elif not workspace.is_contiguous() or workspace.get_device() != index:
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+    wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    st = None if plain and o.is_contiguous() else _strides_of(q, o)
+    _call(_lib.attn_q8_decode, "attn_q8_decode", index, stream, cache.ref, qp, op, ep, lp, H, Tq,
+          1.0 / math.sqrt(D) if scale is None else float(scale), st, opts, wp, wn)
+    _used_on(stream, index, *made)
     return o, lse
 
 
@@ -709,23 +747,21 @@ def attn_q8_select(q, cache, lens, n: int, blocks=None, stream=None):
     """The n closed blocks that each query of q (as in attn_q8_decode) is
     likely to attend to most, by a bound on their keys' products with it:
     int32 [B, H, Tq, n], ascending, -1 behind the last."""
-    torch = _torch()
-    device = _check_cache(cache)
-    B, Hq, Tq, D = _shape4(q)
+    i32 = _torch().int32
+    index = _check_cache(cache)
+    _, H, Tq, _ = _shape4(q)
     shape = (cache.B, cache.H, Tq, int(n))
-    new = blocks is None
-    blocks = torch.empty(shape, dtype=torch.int32, device=device) if new else blocks
-    qp = _check_view(q, "q", (cache.B, Hq, Tq, cache.D))
-    lp = _check(lens, "lens", torch.int32, (cache.B,))
-    bp = _check(blocks, "blocks", torch.int32, shape)
-    for t, name in ((q, "q"), (lens, "lens"), (blocks, "blocks")):
-        _check_on(t, name, device)
+    qp = _view(q, "q", (cache.B, H, Tq, cache.D), index)
+    lp = _whole(lens, "lens", i32, (cache.B,), index)
+    made = []
+    if blocks is None:
+        if n < 1:
+            raise AttnError(-2, "attn_q8_select")
+        made.append(blocks := lens.new_empty(shape))
+    bp = _whole(blocks, "blocks", i32, shape, index)
     st = None if q.is_contiguous() else _strides_of(q)
-    with _device(device):
-        _raise(_lib.attn_q8_select(cache.ref, qp, lp, bp, int(n), Hq, Tq, st, _stream_handle(stream)),
-               "attn_q8_select")
-        if new:
-            _used_on(stream, device, blocks)
+    _call(_lib.attn_q8_select, "attn_q8_select", index, stream, cache.ref, qp, lp, bp, int(n), H, Tq, st)
+    _used_on(stream, index, *made)
     return blocks
 
 
@@ -740,30 +776,26 @@ def attn_q8_evict(cache, lens, keep: int, sink: int = 0, recent: int = 1, out=No
     moved to the front of ``out`` (None: of the cache itself).  Returns
     (lens_out [B], kept [B, H, keep]: the places the blocks came from, -1
     behind the last)."""
-    torch = _torch()
-    device = _check_cache(cache)
+    i32 = _torch().int32
+    index = _check_cache(cache)
     out = cache if out is None else out
-    _check_cache(out, "out")
-    if out.device != device:
-        raise ValueError(f"out must be on {device}, got {out.device}")
+    if _check_cache(out, "out") != index:
+        raise ValueError(f"out must be on cuda:{index}, got {out.device}")
+    if keep < 1:
+        raise AttnError(-2, "attn_q8_evict")
+    lp = _whole(lens, "lens", i32, (cache.B,), index)
     made = []
     if lens_out is None:
-        made.append(lens_out := torch.empty(cache.B, dtype=torch.int32, device=device))
+        made.append(lens_out := lens.new_empty((cache.B,)))
     if kept is None:
-        made.append(kept := torch.empty((cache.B, cache.H, max(int(keep), 0)), dtype=torch.int32, device=device))
-    lp = _check(lens, "lens", torch.int32, (cache.B,))
-    op = _check(lens_out, "lens_out", torch.int32, (cache.B,))
-    kp = _check(kept, "kept", torch.int32, (cache.B, cache.H, int(keep)))
+        made.append(kept := lens.new_empty((cache.B, cache.H, int(keep))))
     if workspace is None:
-        made.append(workspace := torch.empty(_lib.attn_q8_evict_workspace_bytes(cache.ref), dtype=torch.uint8,
-                                             device=device))
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    for t, name in ((lens, "lens"), (lens_out, "lens_out"), (kept, "kept"), (workspace, "workspace")):
-        _check_on(t, name, device)
-    with _device(device):
-        _raise(_lib.attn_q8_evict(cache.ref, out.ref, lp, op, kp, int(keep), int(sink), int(recent),
-                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                  _stream_handle(stream)), "attn_q8_evict")
-        _used_on(stream, device, *made)
+        made.append(workspace := cache.k_codes.new_empty(attn_q8_evict_workspace_bytes(cache)))
+    elif not workspace.is_contiguous() or workspace.get_device() != index:
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+    op = _whole(lens_out, "lens_out", i32, (cache.B,), index)
+    kp = _whole(kept, "kept", i32, (cache.B, cache.H, int(keep)), index)
+    _call(_lib.attn_q8_evict, "attn_q8_evict", index, stream, cache.ref, out.ref, lp, op, kp, int(keep), int(sink),
+          int(recent), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _used_on(stream, index, *made)
     return lens_out, kept

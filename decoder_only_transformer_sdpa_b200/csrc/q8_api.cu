@@ -139,9 +139,8 @@ ATTN_API int attn_q8_decode(const attn_q8_cache *cache, const void *q, void *o, 
     if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(lens, 4)) return ATTN_ERR_ALIGN;
     if ((st = operand(strides, H, Tq, c.D, d.sq)) != ATTN_OK) return st;
     if ((st = operand(strides ? strides + 1 : nullptr, H, Tq, c.D, d.so)) != ATTN_OK) return st;
-    if (workspace_bytes < q8_decode_workspace(c, H, Tq, d.list_n, d.weight != 0) || !workspace ||
-        !aligned(workspace, 256))
-        return ATTN_ERR_WORKSPACE;
+    const size_t need = q8_decode_workspace(c, H, Tq, d.list_n, d.weight != 0);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return ATTN_ERR_WORKSPACE;
     int *err = nullptr;
     if ((st = device_setup(&err)) != ATTN_OK) return st;
     d.q = static_cast<const __nv_bfloat16 *>(q);

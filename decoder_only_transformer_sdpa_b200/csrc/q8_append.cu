@@ -21,14 +21,35 @@ using namespace q8;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-__device__ __forceinline__ uint32_t code_of(float x, float most) { return (uint32_t)(128 + code_number(x, most)); }
-
-__device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of bf16 pairs; NaN stays
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// The larger |x| of a pair as its 15 bits, which grow with it; infinities and NaN come out on top.
+__device__ __forceinline__ uint32_t top(uint32_t pair) {
+    return max(pair & 0x7fffu, (pair >> 16) & 0x7fffu);
+}
+// Byte y of four words as a word, for y = 0 .. 3.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
+    const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[2], w[3], 0x5140);
+    const uint32_t c = __byte_perm(w[0], w[1], 0x7362), d = __byte_perm(w[2], w[3], 0x7362);
+    w[0] = __byte_perm(a, b, 0x5410);
+    w[1] = __byte_perm(a, b, 0x7632);
+    w[2] = __byte_perm(c, d, 0x5410);
+    w[3] = __byte_perm(c, d, 0x7632);
+}
 
 template <int D>
 struct AppendSmem {
-    uint32_t v[D][kBlock / 4 + 1];  // values' codes, four tokens a word
-    uint32_t lo[kWarps][D / 4], hi[kWarps][D / 4];
+    // values' codes, [token][channel]; the pad puts tokens eight apart on few banks' distance
+    alignas(16) uint8_t v[kBlock][D + 8];
+    uint32_t lo[kWarps][D / 2], hi[kWarps][D / 2];  // each warp's smallest and largest keys, bf16 pairs
     uint32_t most[2][kWarps];
 };
 
@@ -38,9 +59,9 @@ __global__ void __launch_bounds__(kThreads)
                   const __nv_bfloat16 *__restrict__ v, const TStrides sv, int n,
                   const int32_t *__restrict__ lens, const int32_t *__restrict__ new_lens, int touched,
                   int *err) {
-    constexpr int kChunks = D / 8;                         // 16-byte chunks of a token
-    constexpr int kPer = kBlock * kChunks / kThreads;      // chunks of a thread
-    constexpr int kQuads = (D / 2) * (kBlock / 4) / kThreads;  // (channel pair, four tokens) of a thread
+    constexpr int kChunks = D / 8;                     // 16-byte chunks of a token
+    constexpr int kPer = kBlock * kChunks / kThreads;  // chunks of a thread: the same channels of every kStep-th token
+    constexpr int kStep = kThreads / kChunks;
     __shared__ AppendSmem<D> sm;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const long long bh = blockIdx.x / touched;
@@ -66,123 +87,117 @@ __global__ void __launch_bounds__(kThreads)
     if (block < closed) {
         const int p0 = block * kBlock;
         ATTN_DCHECK(block < c.blocks && p0 + kBlock <= L, err);
-        // ---- load: keys by 16-byte chunks of a token, values by channel pairs of four tokens
-        uint4 kx[kPer];
-        uint32_t vx[kQuads][4];
+        // ---- load
+        const int t0 = tid / kChunks, ch = 8 * (tid % kChunks);
+        uint4 kx[kPer], vx[kPer];
+        if (p0 >= start) {
+            const __nv_bfloat16 *ks = kr + (long long)(p0 - start + t0) * sk.t + ch;
+            const __nv_bfloat16 *vs = vr + (long long)(p0 - start + t0) * sv.t + ch;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int e = tid + i * kThreads, t = e / kChunks, ch = 8 * (e % kChunks);
-            const int p = p0 + t;
-            const __nv_bfloat16 *src = p < start ? rk + (p % kRing) * D : kr + (long long)(p - start) * sk.t;
-            kx[i] = *reinterpret_cast<const uint4 *>(src + ch);
-        }
+            for (int i = 0; i < kPer; ++i) {
+                kx[i] = *reinterpret_cast<const uint4 *>(ks + i * kStep * sk.t);
+                vx[i] = *reinterpret_cast<const uint4 *>(vs + i * kStep * sv.t);
+            }
+        } else {  // some of the tokens came earlier
 #pragma unroll
-        for (int i = 0; i < kQuads; ++i) {
-            const int e = tid + i * kThreads, cp = e % (D / 2), quad = e / (D / 2);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int p = p0 + 4 * quad + x;
-                const __nv_bfloat16 *src = p < start ? rv + (p % kRing) * D : vr + (long long)(p - start) * sv.t;
-                vx[i][x] = *reinterpret_cast<const uint32_t *>(src + 2 * cp);
+            for (int i = 0; i < kPer; ++i) {
+                const int p = p0 + t0 + i * kStep;
+                const bool old = p < start;
+                kx[i] = *reinterpret_cast<const uint4 *>((old ? rk + (p % kRing) * D : kr + (long long)(p - start) * sk.t) + ch);
+                vx[i] = *reinterpret_cast<const uint4 *>((old ? rv + (p % kRing) * D : vr + (long long)(p - start) * sv.t) + ch);
             }
         }
-        // ---- the two maxima, on the bits: |x| as a 15-bit number grows with |x|, and infinities and NaN
-        // come out on top
-        uint32_t mk = 0, mv = 0;
+        // ---- the smallest and largest key of each channel, the largest |value|
+        uint32_t lo[4] = {kx[0].x, kx[0].y, kx[0].z, kx[0].w}, hi[4] = {kx[0].x, kx[0].y, kx[0].z, kx[0].w};
+        uint32_t va = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            mk = abs_max2(abs_max2(abs_max2(abs_max2(mk, kx[i].x), kx[i].y), kx[i].z), kx[i].w);
+        for (int i = 0; i < kPer; ++i) {
+            const uint32_t kw[4] = {kx[i].x, kx[i].y, kx[i].z, kx[i].w}, vw[4] = {vx[i].x, vx[i].y, vx[i].z, vx[i].w};
 #pragma unroll
-        for (int i = 0; i < kQuads; ++i)
+            for (int x = 0; x < 4; ++x) {
+                if (i > 0) {
+                    lo[x] = min2(lo[x], kw[x]);
+                    hi[x] = max2(hi[x], kw[x]);
+                }
+                va = max2(va, vw[x] & 0x7fff7fffu);
+            }
+        }
+        uint32_t mk = 0;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) mv = abs_max2(mv, vx[i][x]);
-        mk = __reduce_max_sync(0xffffffffu, max(mk & 0xffffu, mk >> 16));
-        mv = __reduce_max_sync(0xffffffffu, max(mv & 0xffffu, mv >> 16));
+        for (int x = 0; x < 4; ++x) mk = max(mk, max(top(lo[x]), top(hi[x])));
+        mk = __reduce_max_sync(0xffffffffu, mk);
+        const uint32_t mv_warp = __reduce_max_sync(0xffffffffu, top(va));
         if (lane == 0) {
             sm.most[0][warp] = mk;
-            sm.most[1][warp] = mv;
+            sm.most[1][warp] = mv_warp;
+        }
+        // (the lanes of a warp with the same channels)
+#pragma unroll
+        for (int off = kChunks; off < 32; off <<= 1)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                lo[x] = min2(lo[x], __shfl_xor_sync(0xffffffffu, lo[x], off));
+                hi[x] = max2(hi[x], __shfl_xor_sync(0xffffffffu, hi[x], off));
+            }
+        if (lane < kChunks) {
+            *reinterpret_cast<uint4 *>(&sm.lo[warp][4 * lane]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4 *>(&sm.hi[warp][4 * lane]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         }
         __syncthreads();
+        uint32_t mv = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             mk = max(mk, sm.most[0][w]);
             mv = max(mv, sm.most[1][w]);
         }
         const bool bad_k = mk >= 0x7f80u, bad_v = mv >= 0x7f80u;
+        const bool none_k = mk == 0 || bad_k, none_v = mv == 0 || bad_v;  // all codes are 128
         const float most_k = __uint_as_float(mk << 16), most_v = __uint_as_float(mv << 16);
+        const Coder code_k(none_k ? 1.f : most_k), code_v(none_v ? 1.f : most_v);
         const long long at = bh * c.blocks + block;
-        // ---- keys
-        uint8_t *kc = c.k_codes + at * (kBlock * D);
-        uint32_t lo[2] = {0xffffffffu, 0xffffffffu}, hi[2] = {0u, 0u};
+        uint8_t *kc = c.k_codes + at * (kBlock * D), *vc = c.v_codes + at * (kBlock * D);
+        // ---- the codes: keys straight to their place, values by way of shared memory
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int e = tid + i * kThreads, t = e / kChunks, ch = 8 * (e % kChunks);
-            const __nv_bfloat162 *x2 = reinterpret_cast<const __nv_bfloat162 *>(&kx[i]);
-            uint32_t w[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const float2 f0 = __bfloat1622float2(x2[2 * x]), f1 = __bfloat1622float2(x2[2 * x + 1]);
-                w[x] = 0x80808080u;
-                if (mk != 0 && !bad_k)
-                    w[x] = code_of(f0.x, most_k) | (code_of(f0.y, most_k) << 8) | (code_of(f1.x, most_k) << 16) |
-                           (code_of(f1.y, most_k) << 24);
-                lo[x] = __vminu4(lo[x], w[x]);
-                hi[x] = __vmaxu4(hi[x], w[x]);
-            }
-            *reinterpret_cast<uint2 *>(kc + key_offset<D>(t, ch)) = make_uint2(w[0], w[1]);
-        }
-        // a warp's lanes with the same channels, then the warps
-#pragma unroll
-        for (int off = kChunks; off < 32; off <<= 1)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                lo[x] = __vminu4(lo[x], __shfl_xor_sync(0xffffffffu, lo[x], off));
-                hi[x] = __vmaxu4(hi[x], __shfl_xor_sync(0xffffffffu, hi[x], off));
-            }
-        if (lane < kChunks) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                sm.lo[warp][2 * lane + x] = lo[x];
-                sm.hi[warp][2 * lane + x] = hi[x];
-            }
-        }
-        // ---- values: four tokens of a channel a word, turned over in shared memory
-#pragma unroll
-        for (int i = 0; i < kQuads; ++i) {
-            const int e = tid + i * kThreads, cp = e % (D / 2), quad = e / (D / 2);
-            uint32_t w0 = 0x80808080u, w1 = 0x80808080u;
-            if (mv != 0 && !bad_v) {
-                w0 = w1 = 0;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&vx[i][x]));
-                    w0 |= code_of(f.x, most_v) << (8 * x);
-                    w1 |= code_of(f.y, most_v) << (8 * x);
-                }
-            }
-            sm.v[2 * cp][quad] = w0;
-            sm.v[2 * cp + 1][quad] = w1;
-        }
-        __syncthreads();
-        uint8_t *vc = c.v_codes + at * (kBlock * D);
-        for (int e = tid; e < D * (kBlock / 16); e += kThreads) {
-            const int ch = e / (kBlock / 16), q = 4 * (e % (kBlock / 16));
-            *reinterpret_cast<uint4 *>(vc + ch * kBlock + 4 * q) =
-                make_uint4(sm.v[ch][q], sm.v[ch][q + 1], sm.v[ch][q + 2], sm.v[ch][q + 3]);
+            uint2 kw = make_uint2(0x80808080u, 0x80808080u), vw = kw;
+            if (!none_k) kw = make_uint2(code_k(kx[i].x, kx[i].y), code_k(kx[i].z, kx[i].w));
+            if (!none_v) vw = make_uint2(code_v(vx[i].x, vx[i].y), code_v(vx[i].z, vx[i].w));
+            *reinterpret_cast<uint2 *>(kc + key_offset<D>(t0 + i * kStep, ch)) = kw;
+            *reinterpret_cast<uint2 *>(&sm.v[t0 + i * kStep][ch]) = vw;
         }
         if (c.bounds && tid < D / 2) {
-            const int x = tid % (D / 4);
-            const bool high = tid >= D / 4;
-            uint32_t r = high ? 0u : 0xffffffffu;
+            // the codes grow with the keys, so the outermost keys have the outermost codes
+            uint32_t l = sm.lo[0][tid], h = sm.hi[0][tid];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) r = high ? __vmaxu4(r, sm.hi[w][x]) : __vminu4(r, sm.lo[w][x]);
-            // code - 128 as a signed byte
-            reinterpret_cast<uint32_t *>(c.bounds + at * (2 * D))[(high ? D / 4 : 0) + x] = r ^ 0x80808080u;
+            for (int w = 1; w < kWarps; ++w) {
+                l = min2(l, sm.lo[w][tid]);
+                h = max2(h, sm.hi[w][tid]);
+            }
+            const uint32_t word = none_k ? 0u : code_k(l, h) ^ 0x80808080u;  // code - 128 as signed bytes
+            uint16_t *to = reinterpret_cast<uint16_t *>(c.bounds + at * (2 * D));
+            to[tid] = (uint16_t)word;
+            to[D / 2 + tid] = (uint16_t)(word >> 16);
+        }
+        __syncthreads();
+        // four channels of eight tokens a thread; eight threads with consecutive tokens fill a channel's 64 bytes
+        for (int e = tid; e < 2 * D; e += kThreads) {
+            const int t = 8 * (e % 8), c4 = 4 * (e / 8);
+            uint32_t w0[4], w1[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                w0[x] = *reinterpret_cast<const uint32_t *>(&sm.v[t + x][c4]);
+                w1[x] = *reinterpret_cast<const uint32_t *>(&sm.v[t + 4 + x][c4]);
+            }
+            transpose4(w0);
+            transpose4(w1);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<uint2 *>(vc + (c4 + x) * kBlock + t) = make_uint2(w0[x], w1[x]);
         }
         if (tid == 0) {
             const float nan = __int_as_float(0x7fffffff);
-            c.scales[2 * at] = bad_k ? nan : __fdiv_rn(most_k, 127.f);
-            c.scales[2 * at + 1] = bad_v ? nan : __fdiv_rn(most_v, 127.f);
+            reinterpret_cast<float2 *>(c.scales)[at] =
+                make_float2(bad_k ? nan : __fdiv_rn(most_k, 127.f), bad_v ? nan : __fdiv_rn(most_v, 127.f));
             if (c.weight) c.weight[at] = 0.f;
         }
     }

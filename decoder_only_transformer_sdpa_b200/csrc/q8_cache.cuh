@@ -56,20 +56,47 @@ __device__ __forceinline__ int checked_length(const int32_t *lens, int b, int bl
 // byte under 0x64 is 1024 + code, and 1152 is subtracted exactly.
 template <int Half>
 __device__ __forceinline__ uint32_t codes_f16x2(uint32_t w) {
-    uint32_t h;
+    uint32_t h, r;
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(h) : "r"(w), "r"(0x64646464u), "n"(Half ? 0x4342 : 0x4140));
-    uint32_t r;
     asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
     return r;
 }
 
-// rint(127 x / most) for |x| <= most, most > 0 and finite (both bf16).  Above
-// 2^120 both are brought down by 2^10 first, so that 127 x stays finite; that
-// is exact but for values whose quotient rounds to 0 either way.
-__device__ __forceinline__ int code_number(float x, float most) {
-    const float f = most >= 1.329227995784916e36f ? 0.0009765625f : 1.f;
-    return __float2int_rn(__fdiv_rn(127.f * (x * f), most * f));
-}
+// Codes of numbers against one maximum `most` (bf16, positive and finite):
+// rint(127 x / most) for |x| <= most, ties to even, without a division each.
+// With f = 2^-e that brings most near 1 (so that nothing below over- or
+// underflows), a = 127 f x and d = f most are exact, and with the rounded
+// reciprocal c of d
+//   t = c a is off by at most 2^-22 t,  r = a - t d is exact (the leading bits
+//   cancel),  t + c r is the quotient but for its last rounding
+// (a residual correction, as in Markstein's division).  A quotient half-way
+// between two whole numbers has at most eight bits, so it comes out exactly;
+// any other quotient is further from half-way than 2^-9 of its size.  1.5 2^23
+// + 128 added then leaves code number + 128 in the low byte.
+struct Coder {
+    uint64_t f127, d, c;  // 127 f, -d and c, each as a pair
+    __device__ __forceinline__ explicit Coder(float most) {
+        int e = (int)(__float_as_uint(most) >> 23) - 127;
+        e = max(-120, min(126, e));  // (127 f is finite, and f is no subnormal)
+        const float f = __uint_as_float((uint32_t)(127 - e) << 23), near = most * f, inv = __frcp_rn(near);
+        f127 = sm100::f2pack(127.f * f, 127.f * f);
+        d = sm100::f2pack(-near, -near);
+        c = sm100::f2pack(inv, inv);
+    }
+    // The codes of a bf16 pair in the low bytes of the two words.
+    __device__ __forceinline__ uint2 operator()(uint32_t pair) const {
+        const uint64_t x = sm100::f2pack(__uint_as_float(pair << 16), __uint_as_float(pair & 0xffff0000u));
+        const uint64_t a = sm100::fmul2(f127, x), t = sm100::fmul2(c, a);
+        const uint64_t q = sm100::ffma2(c, sm100::ffma2(t, d, a), t);
+        const float2 r = sm100::f2unpack(sm100::fadd2(q, sm100::f2pack(12583040.f, 12583040.f)));
+        return make_uint2(__float_as_uint(r.x), __float_as_uint(r.y));
+    }
+    // Of two pairs, as the bytes of a word.
+    __device__ __forceinline__ uint32_t operator()(uint32_t first, uint32_t second) const {
+        const uint2 a = (*this)(first), b = (*this)(second);
+        return __byte_perm(__byte_perm(a.x, a.y, 0x0040), __byte_perm(b.x, b.y, 0x0040), 0x5410);
+    }
+};
 
 // A float's place in the order of all floats, as an unsigned number (the two
 // zeros are one; NaN comes above everything but kFirst).

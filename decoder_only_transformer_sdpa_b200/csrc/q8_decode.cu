@@ -15,37 +15,55 @@
 // turn into f16 exactly (|code - 128| <= 127); queries are scaled by a power of
 // two that brings the row's largest value to [2^14, 2^15), which keeps all
 // eight bits of anything down to 2^-31 of it.  P is rounded to f16 (half a
-// step: 2^-11, less than the bf16 output's 2^-9) after scaling by 2^14, so
-// weights down to 2^-28 of the largest keep that precision.  Sums of P, the
-// scores and both accumulators are float32.
+// step: 2^-11, an eighth of the bf16 output's 2^-8) as 2^7 exp(s - m) with a
+// reference m that is at most 2^8 below the running maximum, so that weights
+// down to 2^-21 of the largest keep that precision and those down to 2^-32
+// count.  Sums of P, the scores and both accumulators are float32.
 //
 // What bounds it is the stream of codes, 128 D bytes a block: every warp has a
 // ring of its own in shared memory, filled by bulk copies that its first lane
-// issues, so a warp never waits for another and some 100 to 190 KB are in
-// flight on an SM.  Blocks go to the warps of a row group's CTAs in turn.
-// The open block is read in bf16 from the ring of recent positions, 16 tokens
-// a warp, with exact products and P as the sum of two bf16 numbers.
+// issues (a block a slot, or its keys and its values each at D = 128), so a warp
+// never waits for another and some 100 KB are in flight on an SM.
+//
+// How the work is shared out goes by its size alone (shares_for):
+//   * little work: the CTAs of a cluster share a row tile, each block going to
+//     the next of their warps, and the cluster's first CTA joins the results
+//     through distributed shared memory: one launch;
+//   * much of it: as many CTAs as the GPU holds take equal runs of all blocks of
+//     all row tiles, whatever the sequences' lengths (which only the kernel
+//     knows); a second kernel joins what the runs left of each row tile.
+//
+// The open block comes first, in bf16 from the ring of recent positions, 16
+// tokens a warp, with exact products and P as the sum of two bf16 numbers.
 #include "q8_cache.cuh"
+
+#include <cooperative_groups.h>
 
 namespace attn {
 namespace {
 
 using namespace sm100;
 using namespace q8;
+namespace cg = cooperative_groups;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr float kPShift = 14.f;  // P is held as 2^14 p
+constexpr float kPShift = 7.f;   // P is held as 2^7 exp2(s - m)
+constexpr float kSlack = 8.f;    // how far a score may pass m before m moves
+constexpr int kMaxCluster = 8;   // portable cluster size
+// What a CTA costs beside its blocks, and the joining kernel, in the time a
+// warp takes for a block.
+constexpr int kPerCta = 3;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
         " {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
         " {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -62,43 +80,48 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 w;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(a));
-    return w;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 w;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(a));
-    return w;
-}
-
-// Warps of a CTA and stages of a warp's ring, by head size: 192 KB of rings at
-// D = 64 and 128, 128 KB at D = 32.
-template <int D>
+// Warps of a CTA, slots of a warp's ring (a block, or half of one at D = 128),
+// and CTAs that an SM holds: 168 registers a thread for up to 8 rows, 255 for 16.
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+template <int D, int NT>
 struct Cfg {
-    static constexpr int kWarps = D == 128 ? 6 : 8;
-    static constexpr int kStages = D == 128 ? 2 : (D == 64 ? 3 : 4);
+    static constexpr int kCtas = NT == 1 ? 3 : 2;
+    static constexpr int kHalves = D == 128 ? 2 : 1;  // slots of a block
+    static constexpr int kSlots = D == 32 ? 4 : (NT == 1 ? 2 : 3);
+    static constexpr bool kQueriesInSmem = NT == 2;  // else in registers
 };
 
-// Layout of the workspace: each CTA's unnormalised output and its running
-// maximum (log2 units) and sum per row, then each block's log2-sum per row
-// (only when the blocks' weights are kept).
+// Layout of the workspace: what each run left of a row tile (its unnormalised
+// output, and its maximum in log2 units and sum per row), at place `run + tile`,
+// which no other pair of the two has, as runs and row tiles follow one another;
+// and each block's log2-sum per row, when the blocks' weights are kept.
 struct Parts {
-    float *o;    // [tile][split][rows][D]
-    float2 *ml;  // [tile][split][rows]
+    float *o;    // [run + tile][rows][D]
+    float2 *ml;  // [run + tile][rows]
+    float *total;  // [tile][rows] log2 of each row's sum (with weights)
     float *lb;   // [B * Hkv][R][blocks]
 };
 
 template <int D, int NT>
 struct Smem {
     static constexpr int kRows = 8 * NT;
-    static constexpr int kStage = 2 * kBlock * D;
+    static constexpr int kSlots = Cfg<D, NT>::kSlots;
+    static constexpr int kSlot = 2 * kBlock * D / Cfg<D, NT>::kHalves;
     static constexpr int kPitch = D + 4;  // rows of partial outputs: four rows apart are on other banks
-    // the rings, then (once they are empty) [warp][row][kPitch] partial outputs
-    alignas(128) uint8_t ring[Cfg<D>::kWarps][Cfg<D>::kStages][kStage];
-    uint64_t full[Cfg<D>::kWarps][Cfg<D>::kStages];
-    float m[Cfg<D>::kWarps][kRows], l[Cfg<D>::kWarps][kRows];
+    // the rings; once they are empty, the warps' outputs and then the CTA's
+    union {
+        alignas(128) uint8_t ring[kWarps][kSlots][kSlot];
+        struct {
+            float part[kWarps][kRows][kPitch];
+            float o[kRows][D];
+        };
+    };
+    uint2 q[Cfg<D, NT>::kQueriesInSmem ? NT : 1][Cfg<D, NT>::kQueriesInSmem ? D / 16 : 1][32];  // fragments
+    uint64_t full[kWarps][kSlots];
+    float m[kWarps][kRows], l[kWarps][kRows];
+    float mc[kRows], lc[kRows];  // the CTA's maximum and sum
+    float total[kRows];          // log2 of each row's sum (for the blocks' weights)
     int abort;
 };
 
@@ -115,7 +138,9 @@ struct DecodeArgs {
     int H, G, Tq;   // query heads, heads of a group, new tokens
     int rows;       // rows of a group: G * Tq, or G with lists (a group is then one token)
     int tiles;      // row tiles of a group
-    int splits;     // CTAs that share a row tile
+    int cluster;    // CTAs of a cluster, which share a row tile; 0: no clusters, but
+    int runs;       // this many runs
+    bool weigh;     // the decode kernel writes the blocks' weights
     float qscale;   // scale * log2(e)
     int weight;     // 0: not kept, 1: set, 2: add
     Parts part;
@@ -141,6 +166,82 @@ __device__ __forceinline__ Where where(const DecodeArgs &a, unsigned index) {
     w.h = (int)(grp % a.c.H);
     return w;
 }
+// ---- runs.  All row tiles' work is laid end to end in units of a block's time:
+// kPad units that stand for what a CTA spends on a row tile beside its blocks,
+// the places of the list or the closed blocks, and kOpen units for an open block.
+// Run r takes the units from r * units_of_run on.  A row tile without a block is
+// nobody's.
+constexpr int kPad = 4, kOpen = 2;
+__device__ __forceinline__ unsigned units_of(const DecodeArgs &a, int b) {
+    int L = a.lens[b];
+    if (L < 0 || L / kBlock > a.c.blocks) L = 0;
+    const int places = a.list ? a.list_n : L / kBlock;
+    return L == 0 ? 0u : (unsigned)(kPad + places + (L % kBlock != 0 ? kOpen : 0));
+}
+__device__ __forceinline__ unsigned tiles_of_sequence(const DecodeArgs &a) {
+    return (unsigned)(a.c.H * (a.list ? a.Tq : 1) * a.tiles);
+}
+// Inclusive sum over the lanes.
+__device__ __forceinline__ unsigned sum_up_to(unsigned x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+    }
+    return x;
+}
+// Units of a run (all units are below 2^31, which the host sees to); `mine`:
+// units_of sequence `lane`.  The whole warp calls it.
+__device__ __forceinline__ unsigned units_of_run(const DecodeArgs &a, unsigned mine) {
+    unsigned all = mine;
+    for (int i = 32 + (threadIdx.x & 31); i < a.c.B; i += 32) all += units_of(a, i);
+    all = __reduce_add_sync(0xffffffffu, all) * tiles_of_sequence(a);
+    return max(1u, (all + a.runs - 1) / (unsigned)a.runs);
+}
+// The row tile with unit u, and u's place in it and the tile's units; false: u
+// lies behind all of them.  The whole warp calls it.
+__device__ __forceinline__ bool tile_at(const DecodeArgs &a, unsigned mine, unsigned u, unsigned &group, unsigned &at,
+                                        unsigned &units) {
+    const int lane = threadIdx.x & 31;
+    const unsigned per = tiles_of_sequence(a);
+    unsigned before = 0;
+    for (int b0 = 0; b0 < a.c.B; b0 += 32) {
+        const unsigned n = b0 == 0 ? mine : (b0 + lane < a.c.B ? units_of(a, b0 + lane) : 0u);
+        const unsigned upto = before + sum_up_to(n);
+        const unsigned in = __ballot_sync(0xffffffffu, u < upto * per);
+        if (in) {
+            const int src = __ffs(in) - 1;
+            units = __shfl_sync(0xffffffffu, n, src);
+            u -= (__shfl_sync(0xffffffffu, upto, src) - units) * per;
+            const unsigned tile = u / units;
+            group = (unsigned)(b0 + src) * per + tile;
+            at = u - tile * units;
+            return true;
+        }
+        before = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return false;
+}
+// The runs with units of row tile `group` that it leaves something of: first ..
+// last, none where last < first.  The whole warp calls it.
+__device__ __forceinline__ void runs_of_tile(const DecodeArgs &a, unsigned group, int &first, int &last) {
+    const int lane = threadIdx.x & 31;
+    const unsigned per = tiles_of_sequence(a);
+    const int b = (int)(group / per);
+    const unsigned each = units_of_run(a, lane < a.c.B ? units_of(a, lane) : 0u);
+    unsigned before = 0;
+    for (int i = lane; i < b; i += 32) before += units_of(a, i);
+    before = __reduce_add_sync(0xffffffffu, before) * per;
+    const unsigned n = units_of(a, b);
+    first = 0;
+    last = -1;
+    if (n == 0) return;
+    const unsigned u0 = before + (group - b * per) * n;
+    first = (int)((u0 + kPad) / each);
+    last = (int)((u0 + n - 1) / each);
+}
+
 // Head in the group and token of row `row` of a group.
 __device__ __forceinline__ int row_head(const DecodeArgs &a, int row) { return a.list ? row : row / a.Tq; }
 __device__ __forceinline__ int row_token(const DecodeArgs &a, const Where &w, int row) {
@@ -155,42 +256,55 @@ struct State {
     float o[D / 16][NT][4];
 };
 
-// Folds scores s[i][nt] (log2 units; -inf where masked) of 16 * Tiles tokens
-// into the running maximum and replaces them by 2^14 exp2(s - max).  Returns
-// the sums of this lane's weights in `sum`.
+// Folds the scores f * s[i][nt] (log2 units, f >= 0; s = -inf where masked) of
+// 16 * Tiles tokens into the running softmax and replaces them by
+// 2^7 exp2(f s - m); the sums of this lane's weights go to `sum`.  The
+// reference m moves (to the maximum so far) only when a score passes it by more
+// than kSlack, which after the first blocks hardly happens: one vote a block
+// instead of two butterflies.
 template <int D, int NT, int Tiles>
-__device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&s)[Tiles][NT][4], float (&sum)[NT][2]) {
+__device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&s)[Tiles][NT][4], const float (&f)[NT][2],
+                                             float (&sum)[NT][2]) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        float base[2], alpha[2];
+        float mx[2];
+        bool past = false;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            float mx = s[0][nt][x];
+            mx[x] = fmaxf(s[0][nt][x], s[0][nt][x + 2]);
 #pragma unroll
-            for (int i = 0; i < Tiles; ++i) mx = fmaxf(mx, fmaxf(s[i][nt][x], s[i][nt][x + 2]));
+            for (int i = 1; i < Tiles; ++i) mx[x] = fmaxf(mx[x], fmaxf(s[i][nt][x], s[i][nt][x + 2]));
+            mx[x] *= f[nt][x];
+            past = past || mx[x] > st.m[nt][x] + kSlack;
+        }
+        if (__any_sync(0xffffffffu, past)) {
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            const float m_new = fmaxf(st.m[nt][x], mx);
-            const float safe = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet
-            alpha[x] = ex2(st.m[nt][x] - safe);
-            base[x] = safe - kPShift;
-            st.m[nt][x] = m_new;
-            sum[nt][x] = 0.f;
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], off));
+                const float m_new = fmaxf(st.m[nt][x], mx[x]);
+                const float alpha = m_new == -INFINITY ? 1.f : ex2(st.m[nt][x] - m_new);
+                st.m[nt][x] = m_new;
+                st.l[nt][x] *= alpha;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    st.o[i][nt][x] *= alpha;
+                    st.o[i][nt][x + 2] *= alpha;
+                }
+            }
         }
 #pragma unroll
-        for (int i = 0; i < Tiles; ++i)
+        for (int x = 0; x < 2; ++x) {
+            const float base = (st.m[nt][x] == -INFINITY ? 0.f : st.m[nt][x]) - kPShift;  // (nothing seen yet)
+            float t = 0.f;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                s[i][nt][x] = ex2(s[i][nt][x] - base[x & 1]);
-                sum[nt][x & 1] += s[i][nt][x];
+            for (int i = 0; i < Tiles; ++i) {
+                s[i][nt][x] = ex2(fmaf(s[i][nt][x], f[nt][x], -base));
+                s[i][nt][x + 2] = ex2(fmaf(s[i][nt][x + 2], f[nt][x], -base));
+                t += s[i][nt][x] + s[i][nt][x + 2];
             }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) st.l[nt][x] = fmaf(st.l[nt][x], alpha[x], sum[nt][x]);
-        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) st.o[i][nt][x] *= alpha[x & 1];
+            sum[nt][x] = t;
+            st.l[nt][x] += t;
         }
     }
 }
@@ -210,503 +324,702 @@ __device__ __forceinline__ void load_row(uint32_t (&w)[D / 8], const __nv_bfloat
     }
 }
 
-// 16 tokens of the open block, positions p0 .. p0 + 15 of a sequence of length L.
+__device__ __forceinline__ void load_transposed(uint32_t (&r)[4], const void *row) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_u32(row))
+                 : "memory");
+}
+// A pair of bf16 numbers with what lies behind the end, infinities and NaN
+// replaced by 0; the latter are noted in `odd`.
+__device__ __forceinline__ uint32_t clean_pair(uint32_t w, bool first, bool second, bool &odd) {
+    w &= (first ? 0xffffu : 0u) | (second ? 0xffff0000u : 0u);
+    if ((w & 0x7f80u) == 0x7f80u) {
+        odd = true;
+        w &= 0xffff0000u;
+    }
+    if ((w & 0x7f800000u) == 0x7f800000u) {
+        odd = true;
+        w &= 0xffffu;
+    }
+    return w;
+}
+
+// 16 tokens of the open block, positions p0 .. p0 + 15 of a sequence of length
+// L: keys k and values v [16][D] in shared memory.
 template <int D, int NT>
-__device__ __forceinline__ void open_tokens(State<D, NT> &st, const DecodeArgs &a, const Where &w,
-                                            const __nv_bfloat16 *(&qrow)[NT], const int (&sees)[NT][2], int p0,
-                                            int L, int lane) {
+__device__ __forceinline__ void open_tokens(State<D, NT> &st, float qscale, const __nv_bfloat16 *(&qrow)[NT],
+                                            const int (&sees)[NT][2], const __nv_bfloat16 *k, const __nv_bfloat16 *v,
+                                            int p0, int L, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    const __nv_bfloat16 *rk = a.c.recent_k + w.bh * kRing * D, *rv = a.c.recent_v + w.bh * kRing * D;
-    float s[1][NT][4];
+    float s[1][NT][4], f[NT][2], sum[NT][2];
+    {
+        uint32_t k0[D / 8], k1[D / 8];  // tokens p0 + g and p0 + g + 8
+        load_row<D>(k0, k + g * D, t);
+        load_row<D>(k1, k + (g + 8) * D, t);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) s[0][nt][0] = s[0][nt][1] = s[0][nt][2] = s[0][nt][3] = 0.f;
-    uint32_t k0[D / 8], k1[D / 8];  // tokens p0 + g and p0 + g + 8
+        for (int nt = 0; nt < NT; ++nt) {
+            uint32_t q[D / 8];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) k0[i] = k1[i] = 0;
-    if (p0 + g < L) load_row<D>(k0, rk + ((p0 + g) % kRing) * D, t);
-    if (p0 + g + 8 < L) load_row<D>(k1, rk + ((p0 + g + 8) % kRing) * D, t);
-    // values: the pairs of tokens (2t, 2t + 1) and (2t + 8, 2t + 9) of channels 16 i + g and + 8; rows past the
-    // end are not read
-    uint32_t va[D / 16][4];
-    uint32_t odd = 0;  // an infinity or a NaN among them
+            for (int i = 0; i < D / 8; ++i) q[i] = 0;
+            if (qrow[nt]) load_row<D>(q, qrow[nt], t);
+            s[0][nt][0] = s[0][nt][1] = s[0][nt][2] = s[0][nt][3] = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int tok = p0 + 2 * t + (x & 2) * 4, ch = 16 * i + g + (x & 1) * 8;
-            uint32_t lo = 0, hi = 0;
-            if (tok < L) lo = *reinterpret_cast<const uint16_t *>(rv + (tok % kRing) * D + ch);
-            if (tok + 1 < L) hi = *reinterpret_cast<const uint16_t *>(rv + ((tok + 1) % kRing) * D + ch);
-            if ((lo & 0x7f80u) == 0x7f80u) {
-                odd = 1;
-                lo = 0;
+            for (int i = 0; i < D / 16; ++i) {
+                const uint32_t ka[4] = {k0[2 * i], k1[2 * i], k0[2 * i + 1], k1[2 * i + 1]};
+                mma_bf16(s[0][nt], ka, q[2 * i], q[2 * i + 1]);
             }
-            if ((hi & 0x7f80u) == 0x7f80u) {
-                odd = 1;
-                hi = 0;
-            }
-            va[i][x] = lo | (hi << 16);
-        }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        uint32_t q[D / 8];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) q[i] = 0;
-        if (qrow[nt]) load_row<D>(q, qrow[nt], t);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            const uint32_t ka[4] = {k0[2 * i], k1[2 * i], k0[2 * i + 1], k1[2 * i + 1]};
-            mma_bf16(s[0][nt], ka, q[2 * i], q[2 * i + 1]);
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int p = p0 + g + (x & 2) * 4;
-            s[0][nt][x] = p <= sees[nt][x & 1] ? s[0][nt][x] * a.qscale : -INFINITY;
+            for (int x = 0; x < 4; ++x)
+                if (p0 + g + (x & 2) * 4 > sees[nt][x & 1]) s[0][nt][x] = -INFINITY;
+            f[nt][0] = f[nt][1] = qscale;
         }
     }
-    float sum[NT][2];
-    softmax_step<D, NT, 1>(st, s, sum);
+    softmax_step<D, NT, 1>(st, s, f, sum);
+    // P as a bf16 number and what that leaves, another one
+    uint32_t b[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        // P as a bf16 number and what that leaves, another one
-        const uint32_t h0 = pack_bf16x2(s[0][nt][0], s[0][nt][1]), h1 = pack_bf16x2(s[0][nt][2], s[0][nt][3]);
-        const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&h0));
-        const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&h1));
-        const uint32_t r0 = pack_bf16x2(s[0][nt][0] - f0.x, s[0][nt][1] - f0.y);
-        const uint32_t r1 = pack_bf16x2(s[0][nt][2] - f1.x, s[0][nt][3] - f1.y);
-        const uint32_t b0 = transpose8(h0), b1 = transpose8(h1), c0 = transpose8(r0), c1 = transpose8(r1);
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            mma_bf16(st.o[i][nt], va[i], b0, b1);
-            mma_bf16(st.o[i][nt], va[i], c0, c1);
+        for (int y = 0; y < 2; ++y) {
+            const uint32_t h = pack_bf16x2(s[0][nt][2 * y], s[0][nt][2 * y + 1]);
+            const float2 r = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&h));
+            b[nt][y] = transpose8(h);
+            b[nt][2 + y] = transpose8(pack_bf16x2(s[0][nt][2 * y] - r.x, s[0][nt][2 * y + 1] - r.y));
+        }
+    bool odd = false;
+    const int n0 = L - p0 - 2 * t;  // tokens from this lane's first pair on
+    const __nv_bfloat16 *row = v + ((lane & 7) + (lane & 16 ? 8 : 0)) * D + (lane & 8);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+        uint32_t va[4];  // channels 16 i + g, + 8 of tokens 2 t, 2 t + 1; the same of tokens 8 further
+        load_transposed(va, row + 16 * i);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) va[x] = clean_pair(va[x], n0 > (x & 2) * 4, n0 > (x & 2) * 4 + 1, odd);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            mma_bf16(st.o[i][nt], va, b[nt][0], b[nt][1]);
+            mma_bf16(st.o[i][nt], va, b[nt][2], b[nt][3]);
         }
     }
-    if (__any_sync(0xffffffffu, odd != 0)) {
+    if (__any_sync(0xffffffffu, odd)) {
         // Infinities and NaN reach only the rows that see their token: added one by one, never as 0 * inf.
-        for (int y = 0; y < 16; ++y) {
+        for (int y = 0; y < 16 && p0 + y < L; ++y)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int src = 4 * (y & 7) + t;
                 const float pa = __shfl_sync(0xffffffffu, y < 8 ? s[0][nt][0] : s[0][nt][2], src);
                 const float pb = __shfl_sync(0xffffffffu, y < 8 ? s[0][nt][1] : s[0][nt][3], src);
-                if (p0 + y < L) {
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
+                for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const float f = __bfloat162float(rv[((p0 + y) % kRing) * D + 16 * i + g + (x & 2) * 4]);
-                            if ((!isfinite(f)) && p0 + y <= sees[nt][x & 1])
-                                st.o[i][nt][x] = fmaf((x & 1) ? pb : pa, f, st.o[i][nt][x]);
-                        }
-                }
+                    for (int x = 0; x < 4; ++x) {
+                        const float e = __bfloat162float(v[y * D + 16 * i + g + (x & 2) * 4]);
+                        if (!isfinite(e) && p0 + y <= sees[nt][x & 1])
+                            st.o[i][nt][x] = fmaf((x & 1) ? pb : pa, e, st.o[i][nt][x]);
+                    }
             }
-        }
     }
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(32 * Cfg<D>::kWarps) decode_kernel(const __grid_constant__ DecodeArgs a) {
-    using Sm = Smem<D, NT>;
-    constexpr int W = Cfg<D>::kWarps, ST = Cfg<D>::kStages, kThreads = 32 * W;
-    constexpr int S = slab(D);
-    constexpr int kRows = 8 * NT;
-    static_assert(sizeof(float) * kRows * Sm::kPitch <= (size_t)ST * Sm::kStage, "partial outputs fit the rings");
-    extern __shared__ uint8_t smem_raw[];
-    Sm &sm = *reinterpret_cast<Sm *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-    volatile int *abort = &sm.abort;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int g = lane >> 2, t = lane & 3;
-    const unsigned group = blockIdx.x / a.splits;  // (row group, row tile)
-    const int split = (int)(blockIdx.x - group * a.splits);
-    const Where w = where(a, group);
-    if (lane == 0) {
-        for (int s = 0; s < ST; ++s) mbar_init(&sm.full[warp][s], 1);
-        fence_mbar_init();
-    }
-    if (tid == 0) sm.abort = 0;
-    __syncthreads();
-    grid_dep_wait();
-    grid_dep_launch();
-    int L = checked_length(a.lens, w.b, a.c.blocks, a.err);
-    if (L < 0) L = 0;
-
-    // ---- this warp's blocks: `first`, + step, ... below `count` (of all closed blocks, or of the list)
-    const int closed = L / kBlock;
-    const int step = a.splits * W, first = split * W + warp;
-    const int count = a.list ? a.list_n : closed;
-    const int32_t *list = a.list ? a.list + (w.bh * a.Tq + w.r0) * a.list_n : nullptr;
-    const uint8_t *kc = a.c.k_codes + w.bh * a.c.blocks * (long long)(kBlock * D);
-    const uint8_t *vc = a.c.v_codes + w.bh * a.c.blocks * (long long)(kBlock * D);
-    const float2 *scales = reinterpret_cast<const float2 *>(a.c.scales) + w.bh * a.c.blocks;
-    // The block at place i of the list, or -1.  What is not an ascending list of closed blocks ended by -1 is
-    // recorded, and the entry skipped.
-    auto block_at = [&](int i) -> int {
-        if (i >= count) return -1;
-        if (!list) return i;
-        const int id = list[i];
-        if (id < 0) return -1;
-        const int before = i > 0 ? list[i - 1] : -1;
-        if (id >= closed || id <= before || (i > 0 && before < 0)) {
-            if (lane == 0) atomicExch(a.err, kErrLength);
-            return -1;
-        }
-        return id;
-    };
-    auto issue = [&](int stage, int id) {
-        if (lane == 0 && id >= 0) {
-            ATTN_DCHECK(id < a.c.blocks, a.err);
-            uint8_t *dst = sm.ring[warp][stage];
-            mbar_arrive_expect_tx(&sm.full[warp][stage], Sm::kStage);
-            bulk_load(dst, kc + (long long)id * (kBlock * D), kBlock * D, &sm.full[warp][stage]);
-            bulk_load(dst + kBlock * D, vc + (long long)id * (kBlock * D), kBlock * D, &sm.full[warp][stage]);
-        }
-    };
-    int ids[ST];
-    float2 sc[ST];
-#pragma unroll
-    for (int s = 0; s < ST; ++s) {
-        ids[s] = block_at(first + s * step);
-        issue(s, ids[s]);
-        sc[s] = ids[s] >= 0 ? scales[ids[s]] : make_float2(0.f, 0.f);
-    }
-
-    // ---- queries: fragments of this lane's row g of each row tile, and the factors of rows 2t, 2t + 1
-    uint32_t qf[NT][D / 8];
-    const __nv_bfloat16 *qrow[NT];
-    float rowf[NT][2];
-    int sees[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int row = w.tile * kRows + nt * 8 + g;
-        qrow[nt] = nullptr;
-        uint32_t x[D / 8];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) x[i] = 0;
-        if (row < a.rows) {
-            qrow[nt] = a.q + (long long)w.b * a.sq.b + (long long)(w.h * a.G + row_head(a, row)) * a.sq.h +
-                       (long long)row_token(a, w, row) * a.sq.t;
-            load_row<D>(x, qrow[nt], t);
-        }
-        uint32_t mx = 0;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) mx = __vmaxu2(mx, x[i] & 0x7fff7fffu);
-        mx = max(mx & 0xffffu, mx >> 16);
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // 2^e with the largest value in [2^14, 2^15); e within what a float32 power of two and its inverse hold
-        int e = 14 - ((int)(mx >> 7) - 127);
-        e = e > 114 ? 114 : e;
-        const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23) * a.qscale;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x[i]));
-            qf[nt][i] = pack_f16x2(f.x * up, f.y * up);
-        }
-#pragma unroll
-        for (int x2 = 0; x2 < 2; ++x2) {
-            rowf[nt][x2] = __shfl_sync(0xffffffffu, down, 4 * (2 * t + x2));
-            const int r = w.tile * kRows + nt * 8 + 2 * t + x2;
-            sees[nt][x2] = r < a.rows ? L - a.Tq + row_token(a, w, r) : -1;
-        }
-    }
-
-    State<D, NT> st;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        st.m[nt][0] = st.m[nt][1] = -INFINITY;
-        st.l[nt][0] = st.l[nt][1] = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) st.o[i][nt][0] = st.o[i][nt][1] = st.o[i][nt][2] = st.o[i][nt][3] = 0.f;
-    }
-    const int all_see = L - a.Tq;  // positions up to here are seen by every query
-
-    // ---- the closed blocks
-    bool ok = true;
-    uint32_t phase = 0;
-    for (int base = first; base < count && ok; base += ST * step) {
-#pragma unroll
-        for (int s = 0; s < ST; ++s) {
-            const int i = base + s * step;
-            if (i >= count) break;
-            const int id = ids[s];
-            if (id >= 0) {
-                if (!(ok = mbar_wait_warp(&sm.full[warp][s], phase, a.err, abort))) break;
-                const uint32_t kb = smem_u32(sm.ring[warp][s]), vb = kb + kBlock * D;
-                // S^T: four tiles of 16 tokens; row y of tile u is token 16 (y >> 1) + 4 u + (y & 1), row y + 8 the
-                // token two further, which is the order in which a lane's 16 value bytes pair up below
-                float sv[4][NT][4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) sv[u][nt][0] = sv[u][nt][1] = sv[u][nt][2] = sv[u][nt][3] = 0.f;
-                    const int tok = 16 * (g >> 1) + 4 * u + (g & 1);
-#pragma unroll
-                    for (int sl = 0; sl < D / S; ++sl) {
-                        uint32_t r0[S / 16], r1[S / 16];
-                        const uint32_t at = kb + sl * (kBlock * S) + tok * S + t * (S / 4);
-                        if constexpr (S == 64) {
-                            const uint4 x = lds128(at), y = lds128(at + 2 * S);
-                            r0[0] = x.x, r0[1] = x.y, r0[2] = x.z, r0[3] = x.w;
-                            r1[0] = y.x, r1[1] = y.y, r1[2] = y.z, r1[3] = y.w;
-                        } else {
-                            const uint2 x = lds64(at), y = lds64(at + 2 * S);
-                            r0[0] = x.x, r0[1] = x.y;
-                            r1[0] = y.x, r1[1] = y.y;
-                        }
-#pragma unroll
-                        for (int k = 0; k < S / 16; ++k) {
-                            const uint32_t ka[4] = {codes_f16x2<0>(r0[k]), codes_f16x2<0>(r1[k]),
-                                                    codes_f16x2<1>(r0[k]), codes_f16x2<1>(r1[k])};
-                            const int f = 2 * (sl * (S / 16) + k);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma_f16(sv[u][nt], ka, qf[nt][f], qf[nt][f + 1]);
-                        }
-                    }
-                }
-                const float ks = sc[s].x, vs = sc[s].y;
-                const int p0 = id * kBlock;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float f0 = ks * rowf[nt][0], f1 = ks * rowf[nt][1];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) sv[u][nt][x] *= (x & 1) ? f1 : f0;
-                }
-                if (p0 + kBlock - 1 > all_see) {  // only the newest positions are masked
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-#pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                if (p0 + 16 * (g >> 1) + 4 * u + (g & 1) + (x & 2) > sees[nt][x & 1])
-                                    sv[u][nt][x] = -INFINITY;
-                }
-                float sum[NT][2];
-                softmax_step<D, NT, 4>(st, sv, sum);
-                if (a.weight) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            float v = sum[nt][x];
-#pragma unroll
-                            for (int off = 4; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-                            const int row = w.tile * kRows + nt * 8 + 2 * t + x;
-                            if (g == 0 && row < a.rows)
-                                a.part.lb[(w.bh * a.rows + row) * a.c.blocks + id] =
-                                    v == 0.f ? -INFINITY : st.m[nt][x] + log2f(v);
-                        }
-                }
-                uint32_t p[4][NT][2];
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        p[u][nt][0] = transpose8(pack_f16x2(sv[u][nt][0], sv[u][nt][1]));
-                        p[u][nt][1] = transpose8(pack_f16x2(sv[u][nt][2], sv[u][nt][3]));
-                    }
-                // O^T: channels 16 c + g and + 8, the lane's 16 tokens 16 t ..
-#pragma unroll
-                for (int c = 0; c < D / 16; ++c) {
-                    const uint32_t at = vb + (16 * c + g) * kBlock + 16 * t;
-                    const uint4 x = lds128(at), y = lds128(at + 8 * kBlock);
-                    const uint32_t r0[4] = {x.x, x.y, x.z, x.w}, r1[4] = {y.x, y.y, y.z, y.w};
-                    float acc[NT][4];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const uint32_t va[4] = {codes_f16x2<0>(r0[u]), codes_f16x2<0>(r1[u]), codes_f16x2<1>(r0[u]),
-                                                codes_f16x2<1>(r1[u])};
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], va, p[u][nt][0], p[u][nt][1]);
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int x2 = 0; x2 < 4; ++x2) st.o[c][nt][x2] = fmaf(vs, acc[nt][x2], st.o[c][nt][x2]);
-                }
-                __syncwarp();
-            }
-            // the stage is read: the block ST places on comes in (a skipped place leaves its barrier's phase
-            // where it is, so it ends the warp's blocks: lists end at their first -1, and bad entries are errors)
-            ids[s] = id >= 0 ? block_at(i + ST * step) : -1;
-            issue(s, ids[s]);
-            sc[s] = ids[s] >= 0 ? scales[ids[s]] : make_float2(0.f, 0.f);
-        }
-        phase ^= 1;
-    }
-    if (!ok) {
-        // a wait ran out: this warp's copies in flight land before its shared memory is used again
-        if (lane == 0) {
-#pragma unroll
-            for (int s = 0; s < ST; ++s) {
-                if (ids[s] >= 0) mbar_wait_drain(&sm.full[warp][s], phase), mbar_wait_drain(&sm.full[warp][s], phase ^ 1);
-            }
-        }
-        __syncwarp();
-    }
-
-    // ---- the open block, 16 tokens a warp, the last warp of the last CTA first
-    const int open = L - closed * kBlock;
-    for (int u = step - 1 - first; 16 * u < open; u += step)
-        open_tokens<D, NT>(st, a, w, qrow, sees, closed * kBlock + 16 * u, L, lane);
-
-    // ---- the warps' results into one
-    __syncthreads();  // every ring is empty
-    float *part = reinterpret_cast<float *>(&sm.ring[0][0][0]);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            float l = st.l[nt][x];
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-            if (g == 0) {
-                sm.m[warp][nt * 8 + 2 * t + x] = st.m[nt][x];
-                sm.l[warp][nt * 8 + 2 * t + x] = l;
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                part[(warp * kRows + nt * 8 + 2 * t + (x & 1)) * Sm::kPitch + 16 * c + g + (x & 2) * 4] =
-                    st.o[c][nt][x];
-    }
-    __syncthreads();
-    const int here = min(kRows, a.rows - w.tile * kRows);
-    for (int e = tid; e < here * (D / 4); e += kThreads) {
-        const int row = e / (D / 4), ch = 4 * (e % (D / 4));
-        float m = -INFINITY, l = 0.f;
-#pragma unroll
-        for (int y = 0; y < W; ++y) m = fmaxf(m, sm.m[y][row]);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float safe = m == -INFINITY ? 0.f : m;
-#pragma unroll
-        for (int y = 0; y < W; ++y) {
-            const float f = ex2(sm.m[y][row] - safe);
-            const float4 x = *reinterpret_cast<const float4 *>(part + (y * kRows + row) * Sm::kPitch + ch);
-            l = fmaf(f, sm.l[y][row], l);
-            o.x = fmaf(f, x.x, o.x);
-            o.y = fmaf(f, x.y, o.y);
-            o.z = fmaf(f, x.z, o.z);
-            o.w = fmaf(f, x.w, o.w);
-        }
-        const long long at = ((long long)group * a.splits + split) * kRows + row;
-        *reinterpret_cast<float4 *>(a.part.o + at * D + ch) = o;
-        if (ch == 0) a.part.ml[at] = make_float2(m, l);
-    }
+// One result (maximum folded into f, sum l1, output o1) into a joint one.
+__device__ __forceinline__ void join(float4 &o, float &l, float f, float l1, const float4 &o1) {
+    l = fmaf(f, l1, l);
+    o.x = fmaf(f, o1.x, o.x);
+    o.y = fmaf(f, o1.y, o.y);
+    o.z = fmaf(f, o1.z, o.z);
+    o.w = fmaf(f, o1.w, o.w);
 }
 
-// Joins the CTAs of each row tile: o, lse, and with `weight` the blocks'
-// attention weights.  One CTA a row tile (and, with weights, kWeightCtas a key
-// head in blockIdx.y).
-constexpr int kJoinThreads = 128;
-template <int D, int NT>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ DecodeArgs a) {
-    constexpr int kRows = 8 * NT;
-    const int tid = threadIdx.x;
-    grid_dep_wait();
-    grid_dep_launch();
-    const unsigned group = blockIdx.x;
-    const Where w = where(a, group);
-    const int here = min(kRows, a.rows - w.tile * kRows);
-    for (int e = tid; e < here * (D / 4); e += kJoinThreads) {
-        const int row = e / (D / 4), ch = 4 * (e % (D / 4));
-        const long long at = (long long)group * a.splits * kRows + row;
-        float m = -INFINITY, l = 0.f;
-        for (int y = 0; y < a.splits; ++y) m = fmaxf(m, a.part.ml[at + y * kRows].x);
-        const float safe = m == -INFINITY ? 0.f : m;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int y = 0; y < a.splits; ++y) {
-            const float2 ml = a.part.ml[at + y * kRows];
-            const float4 x = *reinterpret_cast<const float4 *>(a.part.o + (at + y * kRows) * D + ch);
-            const float f = ex2(ml.x - safe);
-            l = fmaf(f, ml.y, l);
-            o.x = fmaf(f, x.x, o.x);
-            o.y = fmaf(f, x.y, o.y);
-            o.z = fmaf(f, x.z, o.z);
-            o.w = fmaf(f, x.w, o.w);
-        }
-        const int r = w.tile * kRows + row;
-        const int head = w.h * a.G + row_head(a, r), tok = row_token(a, w, r);
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: zeros
-        *reinterpret_cast<uint2 *>(a.o + (long long)w.b * a.so.b + (long long)head * a.so.h +
-                                   (long long)tok * a.so.t + ch) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (ch == 0)
-            a.lse[((long long)w.b * a.H + head) * a.Tq + tok] =
-                l == 0.f ? -INFINITY : (m + (log2f(l) - kPShift)) * kLn2;
-    }
+// Four channels of row `r` of a group, and with the first ones its lse.
+__device__ __forceinline__ void write_row(const DecodeArgs &a, const Where &w, int r, int ch, float m, float l,
+                                          const float4 &o) {
+    const int head = w.h * a.G + row_head(a, r), tok = row_token(a, w, r);
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: zeros
+    *reinterpret_cast<uint2 *>(a.o + (long long)w.b * a.so.b + (long long)head * a.so.h + (long long)tok * a.so.t +
+                               ch) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (ch == 0)
+        a.lse[((long long)w.b * a.H + head) * a.Tq + tok] = l == 0.f ? -INFINITY : (m + (log2f(l) - kPShift)) * kLn2;
 }
 
-// weight[j] (+)= sum over rows of exp(block j's log-sum - the row's log-sum).
-// blockIdx.x: key head; blockIdx.y: 128 blocks at a time.
-template <int NT>
-__global__ void __launch_bounds__(kJoinThreads) weight_kernel(const __grid_constant__ DecodeArgs a) {
-    constexpr int kRows = 8 * NT;
-    extern __shared__ float total[];  // [rows] log2 of each row's sum
-    grid_dep_wait();
-    grid_dep_launch();
-    const long long bh = blockIdx.x;
-    const int b = (int)(bh / a.c.H);
-    int L = a.lens[b];
-    if (L < 0 || L / kBlock > a.c.blocks) L = 0;  // recorded by the attention
-    const int closed = L / kBlock;
-    if ((int)blockIdx.y * kJoinThreads >= closed) return;
-    for (int row = threadIdx.x; row < a.rows; row += kJoinThreads) {
-        const long long at = ((bh * a.tiles + row / kRows) * a.splits) * kRows + row % kRows;
-        float m = -INFINITY, l = 0.f;
-        for (int y = 0; y < a.splits; ++y) m = fmaxf(m, a.part.ml[at + y * kRows].x);
-        const float safe = m == -INFINITY ? 0.f : m;
-        for (int y = 0; y < a.splits; ++y) {
-            const float2 ml = a.part.ml[at + y * kRows];
-            l = fmaf(ex2(ml.x - safe), ml.y, l);
-        }
-        total[row] = l == 0.f ? INFINITY : m + log2f(l);  // a row that sees nothing gives nothing
-    }
-    __syncthreads();
-    const int j = (int)blockIdx.y * kJoinThreads + threadIdx.x;
-    if (j >= closed) return;
+// log2 of a row's sum, in the units of the blocks' sums; a row that sees nothing gives nothing.
+__device__ __forceinline__ float row_total(float m, float l) { return l == 0.f ? INFINITY : m + log2f(l); }
+
+// weight[j] (+)= sum over the rows of exp(block j's log-sum - the row's log-sum).
+__device__ __forceinline__ void write_weight(const DecodeArgs &a, long long bh, int j, const float *total) {
     float sum = 0.f;
     for (int row = 0; row < a.rows; ++row) sum += ex2(a.part.lb[(bh * a.rows + row) * a.c.blocks + j] - total[row]);
     float *out = a.c.weight + bh * a.c.blocks + j;
     *out = a.weight == 2 ? *out + sum : sum;
 }
 
-// CTAs that share a row tile: enough to fill the GPU's 148 SMs, no more than
-// give every warp a block.
-int splits_for(long long tiles, int D, int blocks) {
-    const int warps = D == 128 ? Cfg<128>::kWarps : Cfg<64>::kWarps;
-    const long long most = (blocks + warps) / warps;  // the open block is a unit of work too
-    long long n = 148 / tiles;
-    n = n < 1 ? 1 : n;
-    return (int)(n > most ? most : n);
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(const __grid_constant__ DecodeArgs a) {
+    using Sm = Smem<D, NT>;
+    constexpr int SL = Sm::kSlots, kRows = Sm::kRows, S = slab(D), kHalves = Cfg<D, NT>::kHalves;
+    constexpr int kSide = kBlock * D;  // bytes of a block's keys, and of its values
+    static_assert(sizeof(float) * kWarps * kRows * Sm::kPitch + sizeof(float) * kRows * D <= sizeof(Sm::ring),
+                  "the outputs take no more than the rings");
+    extern __shared__ uint8_t smem_raw[];
+    Sm &sm = *reinterpret_cast<Sm *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+    volatile int *abort = &sm.abort;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+    if (lane < SL) mbar_init(&sm.full[warp][lane], 1);
+    fence_mbar_init();
+    if (tid == 0) sm.abort = 0;
+    __syncthreads();
+    grid_dep_wait();
+    grid_dep_launch();
+
+    // ---- this CTA's work: with clusters every a.cluster-th kWarps blocks of a row tile, else a run
+    unsigned group, left = 1, skip = 0;  // units still to do, and those of the row tile that are not this CTA's
+    int rank = 0;
+    if (a.cluster) {
+        group = blockIdx.x / a.cluster;
+        rank = (int)(blockIdx.x - group * a.cluster);
+    } else {
+        const unsigned mine = lane < a.c.B ? units_of(a, lane) : 0u;
+        left = units_of_run(a, mine);
+        unsigned units;
+        if (!tile_at(a, mine, blockIdx.x * left, group, skip, units)) return;
+    }
+    int slot = 0, put_slot = 0, ahead = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    while (true) {
+        const Where w = where(a, group);
+        int L = checked_length(a.lens, w.b, a.c.blocks, a.err);
+        if (L < 0) L = 0;
+        // ---- this warp's blocks: places first, first + step, ... below `count` (of all closed blocks, or of the list),
+        // and its tokens of the open block: open_at, + 16 step, ... below `open`
+        const int closed = L / kBlock;
+        int count = a.list ? a.list_n : closed;
+        int step = kWarps, first = warp, open = L - closed * kBlock, open_at = 16 * (kWarps - 1 - warp);
+        if (a.cluster) {
+            step = a.cluster * kWarps;
+            first = rank * kWarps + warp;
+            open_at = 16 * (step - 1 - first);  // the last warp of the last CTA first
+            left = 0;
+        } else {
+            const unsigned units = (unsigned)(kPad + count + (open ? kOpen : 0)), end = min(units, skip + left);
+            left -= end - skip;
+            if (skip > kPad) first += (int)skip - kPad;
+            // the open block goes with the first of its units
+            if (skip > (unsigned)(kPad + count) || end <= (unsigned)(kPad + count)) open = 0;
+            count = min(count, max(0, (int)end - kPad));
+            skip = 0;
+        }
+        const int32_t *list = a.list ? a.list + (w.bh * a.Tq + w.r0) * a.list_n : nullptr;
+        const uint8_t *kc = a.c.k_codes + w.bh * a.c.blocks * (long long)(kBlock * D);
+        const uint8_t *vc = a.c.v_codes + w.bh * a.c.blocks * (long long)(kBlock * D);
+        const float2 *scales = reinterpret_cast<const float2 *>(a.c.scales) + w.bh * a.c.blocks;
+        // The first block at place i or a whole number of steps behind it, or -1.  What is not an ascending list of
+        // closed blocks ended by -1 is recorded, and the entry skipped.
+        auto block_from = [&](int &i) -> int {
+            if (!list) return i < count ? i : -1;
+            for (; i < count; i += step) {
+                const int id = list[i];
+                if (id < 0) continue;
+                const int before = i > 0 ? list[i - 1] : -1;
+                if (id < closed && id > before && !(i > 0 && before < 0)) return id;
+                if (lane == 0) atomicExch(a.err, kErrLength);
+            }
+            return -1;
+        };
+
+        // ---- bulk copies run SL slots ahead of what is read: first 16 tokens of the open block, then the blocks
+        int put_at = first, put_id = block_from(put_at), put_half = 0;
+        auto put = [&]() {
+            if (put_id < 0) return;
+            if (lane == 0) {
+                ATTN_DCHECK(put_id < a.c.blocks && put_slot < SL, a.err);
+                uint8_t *to = sm.ring[warp][put_slot];
+                uint64_t *bar = &sm.full[warp][put_slot];
+                mbar_arrive_expect_tx(bar, Sm::kSlot);
+                const long long from = (long long)put_id * kSide;
+                if (kHalves == 1) {
+                    bulk_load(to, kc + from, kSide, bar);
+                    bulk_load(to + kSide, vc + from, kSide, bar);
+                } else {
+                    bulk_load(to, (put_half ? vc : kc) + from, kSide, bar);
+                }
+            }
+            ++ahead;
+            put_slot = put_slot + 1 == SL ? 0 : put_slot + 1;
+            if (kHalves == 2) put_half ^= 1;
+            if (put_half == 0) {
+                put_at += step;
+                put_id = block_from(put_at);
+            }
+        };
+        auto wait = [&]() { return mbar_wait_warp(&sm.full[warp][slot], phase, a.err, abort); };
+        auto next = [&]() {  // the slot is read: what is SL slots on comes in
+            --ahead;
+            __syncwarp();
+            put();
+            slot = slot + 1 == SL ? 0 : slot + 1;
+            phase ^= slot == 0;
+        };
+        const bool tokens = open_at < open;  // (step is 4 or more: 16 tokens are all of a warp's)
+        if (tokens) {
+            constexpr int kBytes = 16 * D * 2;  // of 16 tokens' keys
+            static_assert(2 * kBytes <= Sm::kSlot, "a slot holds 16 tokens in bf16");
+            if (lane == 0) {
+                const int row = (closed * kBlock + open_at) % kRing;
+                ATTN_DCHECK(row <= kRing - 16, a.err);
+                uint64_t *bar = &sm.full[warp][put_slot];
+                mbar_arrive_expect_tx(bar, 2 * kBytes);
+                bulk_load(sm.ring[warp][put_slot], a.c.recent_k + (w.bh * kRing + row) * D, kBytes, bar);
+                bulk_load(sm.ring[warp][put_slot] + kBytes, a.c.recent_v + (w.bh * kRing + row) * D, kBytes, bar);
+            }
+            ++ahead;
+            put_slot = put_slot + 1 == SL ? 0 : put_slot + 1;
+        }
+#pragma unroll 1
+        for (int s = tokens; s < SL; ++s) put();
+        int at = first, id = block_from(at);
+        float2 sc = id >= 0 ? scales[id] : make_float2(0.f, 0.f);
+
+        // ---- queries: fragments of this lane's row g of each row tile, and the factors of rows 2t, 2t + 1
+        uint32_t qf[Cfg<D, NT>::kQueriesInSmem ? 1 : NT][D / 8];
+        const __nv_bfloat16 *qrow[NT];
+        float rowf[NT][2];
+        int sees[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = w.tile * kRows + nt * 8 + g;
+            qrow[nt] = nullptr;
+            uint32_t x[D / 8];
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) x[i] = 0;
+            if (row < a.rows) {
+                qrow[nt] = a.q + (long long)w.b * a.sq.b + (long long)(w.h * a.G + row_head(a, row)) * a.sq.h +
+                           (long long)row_token(a, w, row) * a.sq.t;
+                load_row<D>(x, qrow[nt], t);
+            }
+            uint32_t mx = 0;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) mx = __vmaxu2(mx, x[i] & 0x7fff7fffu);
+            mx = max(mx & 0xffffu, mx >> 16);
+            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            // 2^e with the largest value in [2^14, 2^15); e within what a float32 power of two and its inverse hold
+            int e = 14 - ((int)(mx >> 7) - 127);
+            e = e > 114 ? 114 : e;
+            const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23) * a.qscale;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x[i]));
+                x[i] = pack_f16x2(f.x * up, f.y * up);
+                if constexpr (!Cfg<D, NT>::kQueriesInSmem) qf[nt][i] = x[i];
+            }
+            if constexpr (Cfg<D, NT>::kQueriesInSmem) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    if (warp == i % kWarps) sm.q[nt][i][lane] = make_uint2(x[2 * i], x[2 * i + 1]);
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                rowf[nt][y] = __shfl_sync(0xffffffffu, down, 4 * (2 * t + y));
+                const int r = w.tile * kRows + nt * 8 + 2 * t + y;
+                sees[nt][y] = r < a.rows ? L - a.Tq + row_token(a, w, r) : -1;
+            }
+        }
+        if constexpr (Cfg<D, NT>::kQueriesInSmem) __syncthreads();
+        auto query = [&](int nt, int i) -> uint2 {
+            if constexpr (Cfg<D, NT>::kQueriesInSmem)
+                return sm.q[nt][i][lane];
+            else
+                return make_uint2(qf[nt][2 * i], qf[nt][2 * i + 1]);
+        };
+
+        State<D, NT> st;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            st.m[nt][0] = st.m[nt][1] = -INFINITY;
+            st.l[nt][0] = st.l[nt][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) st.o[i][nt][0] = st.o[i][nt][1] = st.o[i][nt][2] = st.o[i][nt][3] = 0.f;
+        }
+
+        // ---- the open block
+        if (tokens && (ok = wait())) {
+            const __nv_bfloat16 *k = reinterpret_cast<const __nv_bfloat16 *>(sm.ring[warp][slot]);
+            open_tokens<D, NT>(st, a.qscale, qrow, sees, k, k + 16 * D, closed * kBlock + open_at, L, lane);
+            next();
+        }
+
+        // ---- the closed blocks
+        const int all_see = L - a.Tq;  // positions up to here are seen by every query
+#pragma unroll 1
+        while (id >= 0 && ok) {
+            int at_next = at + step;
+            const int id_next = block_from(at_next);
+            const float2 sc_next = id_next >= 0 ? scales[id_next] : make_float2(0.f, 0.f);
+            if (!(ok = wait())) break;
+            // S^T: four tiles of 16 tokens; row y of tile u is token 16 (y >> 1) + 4 u + (y & 1), row y + 8 the token two
+            // further, which is the order in which a lane's 16 value bytes pair up below
+            float sv[4][NT][4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) sv[u][nt][0] = sv[u][nt][1] = sv[u][nt][2] = sv[u][nt][3] = 0.f;
+#pragma unroll
+            for (int sl = 0; sl < D / S; ++sl) {
+                const uint8_t *kb = sm.ring[warp][slot] + sl * (kBlock * S) + (16 * (g >> 1) + (g & 1)) * S + t * (S / 4);
+#pragma unroll
+                for (int u0 = 0; u0 < 4; u0 += 2) {  // two tiles at a time: 16 registers of codes
+                    uint32_t r0[2][S / 16], r1[2][S / 16];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint8_t *from = kb + 4 * (u0 + u) * S;
+                        if constexpr (S == 64) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(from);
+                            const uint4 y = *reinterpret_cast<const uint4 *>(from + 2 * S);
+                            r0[u][0] = x.x, r0[u][1] = x.y, r0[u][2] = x.z, r0[u][3] = x.w;
+                            r1[u][0] = y.x, r1[u][1] = y.y, r1[u][2] = y.z, r1[u][3] = y.w;
+                        } else {
+                            const uint2 x = *reinterpret_cast<const uint2 *>(from);
+                            const uint2 y = *reinterpret_cast<const uint2 *>(from + 2 * S);
+                            r0[u][0] = x.x, r0[u][1] = x.y;
+                            r1[u][0] = y.x, r1[u][1] = y.y;
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < S / 16; ++k) {
+                        uint32_t ka[2][4];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            ka[u][0] = codes_f16x2<0>(r0[u][k]);
+                            ka[u][1] = codes_f16x2<0>(r1[u][k]);
+                            ka[u][2] = codes_f16x2<1>(r0[u][k]);
+                            ka[u][3] = codes_f16x2<1>(r1[u][k]);
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint2 q = query(nt, sl * (S / 16) + k);
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) mma_f16(sv[u0 + u][nt], ka[u], q.x, q.y);
+                        }
+                    }
+                }
+            }
+            if (kHalves == 2) next();
+            const int p0 = id * kBlock;
+            if (p0 + kBlock - 1 > all_see) {  // only the newest positions are masked
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (p0 + 16 * (g >> 1) + 4 * u + (g & 1) + (x & 2) > sees[nt][x & 1])
+                                sv[u][nt][x] = -INFINITY;
+            }
+            float f[NT][2], sum[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    f[nt][x] = sc.x * rowf[nt][x];
+                    // a block of zeros: any factor gives its scores 0 and keeps -inf what it is (a NaN stays)
+                    if (f[nt][x] == 0.f) f[nt][x] = 1.f;
+                }
+            softmax_step<D, NT, 4>(st, sv, f, sum);
+            if (a.weight) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float v = sum[nt][x];
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+                        const int row = w.tile * kRows + nt * 8 + 2 * t + x;
+                        if (g == 0 && row < a.rows)
+                            a.part.lb[(w.bh * a.rows + row) * a.c.blocks + id] =
+                                v == 0.f ? -INFINITY : st.m[nt][x] + log2f(v);
+                    }
+            }
+            uint32_t p[4][NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    p[u][nt][0] = transpose8(pack_f16x2(sv[u][nt][0], sv[u][nt][1]));
+                    p[u][nt][1] = transpose8(pack_f16x2(sv[u][nt][2], sv[u][nt][3]));
+                }
+            // O^T: channels 16 c + g and + 8, the lane's 16 tokens 16 t ..; a block's sum is scaled as it joins the rest
+            if (kHalves == 2 && !(ok = wait())) break;
+            const uint8_t *vb = sm.ring[warp][slot] + (kHalves == 2 ? 0 : kSide) + g * kBlock + 16 * t;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(vb + 16 * c * kBlock);
+                const uint4 y = *reinterpret_cast<const uint4 *>(vb + (16 * c + 8) * kBlock);
+                const uint32_t r0[4] = {x.x, x.y, x.z, x.w}, r1[4] = {y.x, y.y, y.z, y.w};
+                float acc[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint32_t va[4] = {codes_f16x2<0>(r0[u]), codes_f16x2<0>(r1[u]), codes_f16x2<1>(r0[u]),
+                                            codes_f16x2<1>(r1[u])};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], va, p[u][nt][0], p[u][nt][1]);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int y2 = 0; y2 < 4; ++y2) {
+                        st.o[c][nt][y2] = fmaf(sc.y, acc[nt][y2], st.o[c][nt][y2]);
+                    }
+            }
+            next();
+            at = at_next;
+            id = id_next;
+            sc = sc_next;
+        }
+        if (!ok) {
+            // A wait ran out: this warp's copies in flight land before its shared memory is used again.
+            for (; ahead > 0; --ahead) {
+                if (lane == 0) mbar_wait_drain(&sm.full[warp][slot], phase);
+                slot = slot + 1 == SL ? 0 : slot + 1;
+                phase ^= slot == 0;
+            }
+            __syncwarp();
+        }
+
+        // ---- the warps' results into one
+        __syncthreads();  // every ring is empty
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float l = st.l[nt][x];
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+                if (g == 0) {
+                    sm.m[warp][nt * 8 + 2 * t + x] = st.m[nt][x];
+                    sm.l[warp][nt * 8 + 2 * t + x] = l;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    sm.part[warp][nt * 8 + 2 * t + (x & 1)][16 * c + g + (x & 2) * 4] = st.o[c][nt][x];
+        }
+        __syncthreads();
+        const int here = min(kRows, a.rows - w.tile * kRows);
+        for (int e = tid; e < here * (D / 4); e += kThreads) {
+            const int row = e / (D / 4), ch = 4 * (e % (D / 4));
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int y = 0; y < kWarps; ++y) m = fmaxf(m, sm.m[y][row]);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float safe = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int y = 0; y < kWarps; ++y)
+                join(o, l, ex2(sm.m[y][row] - safe), sm.l[y][row], *reinterpret_cast<const float4 *>(&sm.part[y][row][ch]));
+            if (a.cluster == 1) {
+                write_row(a, w, w.tile * kRows + row, ch, m, l, o);
+            } else if (a.cluster) {
+                *reinterpret_cast<float4 *>(&sm.o[row][ch]) = o;
+            } else {
+                const long long to = ((long long)blockIdx.x + group) * kRows + row;
+                *reinterpret_cast<float4 *>(a.part.o + to * D + ch) = o;
+                if (ch == 0) a.part.ml[to] = make_float2(m, l);
+            }
+            if (a.cluster && ch == 0) {
+                sm.mc[row] = m;
+                sm.lc[row] = l;
+            }
+        }
+        if (!a.cluster) {
+            // ---- the next row tile with units
+            if (left == 0) return;
+            do {
+                if (++group >= (unsigned)a.c.B * tiles_of_sequence(a)) return;
+            } while (units_of(a, where(a, group).b) == 0);
+            __syncthreads();  // the rings take blocks again
+            continue;
+        }
+        // ---- the cluster's results into one, in its first CTA
+        if (a.cluster > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+        if (a.cluster > 1 && rank == 0) {
+            for (int e = tid; e < here * (D / 4); e += kThreads) {
+                const int row = e / (D / 4), ch = 4 * (e % (D / 4));
+                float ms[kMaxCluster];
+                float m = -INFINITY, l = 0.f;
+#pragma unroll
+                for (int y = 0; y < kMaxCluster; ++y) {
+                    ms[y] = y < a.cluster ? *cluster.map_shared_rank(&sm.mc[row], y) : -INFINITY;
+                    m = fmaxf(m, ms[y]);
+                }
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                const float safe = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                for (int y = 0; y < kMaxCluster; ++y)
+                    if (y < a.cluster)
+                        join(o, l, ex2(ms[y] - safe), *cluster.map_shared_rank(&sm.lc[row], y),
+                             *reinterpret_cast<const float4 *>(cluster.map_shared_rank(&sm.o[row][ch], y)));
+                write_row(a, w, w.tile * kRows + row, ch, m, l, o);
+            }
+        }
+        if (a.weigh) {
+            // ---- the weights of this CTA's blocks
+            if (tid < here) {
+                float m = -INFINITY, l = 0.f;
+                for (int y = 0; y < a.cluster; ++y) m = fmaxf(m, *cluster.map_shared_rank(&sm.mc[tid], y));
+                const float safe = m == -INFINITY ? 0.f : m;
+                for (int y = 0; y < a.cluster; ++y)
+                    l = fmaf(ex2(*cluster.map_shared_rank(&sm.mc[tid], y) - safe), *cluster.map_shared_rank(&sm.lc[tid], y), l);
+                sm.total[tid] = row_total(m, l);
+            }
+            __syncthreads();
+            // places rank * kWarps + (0 .. kWarps - 1) + a multiple of step are this CTA's
+            for (int e = tid; (e / kWarps) * step + rank * kWarps < closed; e += kThreads) {
+                const int j = (e / kWarps) * step + rank * kWarps + e % kWarps;
+                if (j < closed) write_weight(a, w.bh, j, sm.total);
+            }
+        }
+        if (a.cluster > 1) cluster.sync();  // the CTAs keep their shared memory until it has been read
+        return;
+    }
+}
+
+// Joins what the runs left of a row: blockIdx.x is its row tile, blockIdx.y its
+// place there.  A row of D / 4 threads takes every kParts-th run.
+constexpr int kJoinThreads = 128;
+template <int D, int NT>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ DecodeArgs a) {
+    constexpr int kRows = 8 * NT, kLanes = D / 4, kParts = kJoinThreads / kLanes;
+    __shared__ float4 so[kParts][kLanes];
+    __shared__ float sl[kParts], sm[kJoinThreads / 32];
+    const int tid = threadIdx.x;
+    const unsigned group = blockIdx.x;
+    const int row = (int)blockIdx.y;
+    const Where w = where(a, group);
+    if (w.tile * kRows + row >= a.rows) return;
+    // The lengths are there: the attention, which does not write them, waited for what came before it.
+    checked_length(a.lens, w.b, a.c.blocks, a.err);  // (a sequence without units is in no run)
+    int first, last;
+    runs_of_tile(a, group, first, last);
+    grid_dep_wait();
+    grid_dep_launch();
+    const float2 *ml = a.part.ml + (long long)group * kRows + row;
+    const float *po = a.part.o + ((long long)group * kRows + row) * D + 4 * (tid % kLanes);
+    float m = -INFINITY;
+    for (int y = first + tid; y <= last; y += kJoinThreads) m = fmaxf(m, ml[(long long)y * kRows].x);
+#pragma unroll
+    for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (tid % 32 == 0) sm[tid / 32] = m;
+    __syncthreads();
+#pragma unroll
+    for (int y = 0; y < kJoinThreads / 32; ++y) m = fmaxf(m, sm[y]);
+    const float safe = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int y = first + tid / kLanes; y <= last; y += kParts) {
+        const float2 x = ml[(long long)y * kRows];
+        join(o, l, ex2(x.x - safe), x.y, *reinterpret_cast<const float4 *>(po + (long long)y * kRows * D));
+    }
+    so[tid / kLanes][tid % kLanes] = o;
+    if (tid % kLanes == 0) sl[tid / kLanes] = l;
+    __syncthreads();
+    if (tid < kLanes) {
+#pragma unroll
+        for (int y = 1; y < kParts; ++y) join(o, l, 1.f, sl[y], so[y][tid]);
+        write_row(a, w, w.tile * kRows + row, 4 * tid, m, l, o);
+        if (tid == 0 && a.weight) a.part.total[(long long)group * kRows + row] = row_total(m, l);
+    }
+}
+
+// The blocks' weights where a key head's rows are joined from runs.
+// blockIdx.x: key head; blockIdx.y: 128 blocks at a time.
+template <int NT>
+__global__ void __launch_bounds__(kJoinThreads) weight_kernel(const __grid_constant__ DecodeArgs a) {
+    constexpr int kRows = 8 * NT;
+    grid_dep_wait();
+    grid_dep_launch();
+    const long long bh = blockIdx.x;
+    int L = a.lens[bh / a.c.H];
+    if (L < 0 || L / kBlock > a.c.blocks) L = 0;  // recorded by the attention
+    const int j = (int)blockIdx.y * kJoinThreads + threadIdx.x;
+    // (a key head's row tiles follow one another, so its rows do too)
+    if (j < L / kBlock) write_weight(a, bh, j, a.part.total + bh * a.tiles * kRows);
+}
+
+constexpr int kSms = 148;
+
+template <int D>
+int ctas_of(int nt) {
+    return kSms * (nt == 1 ? Cfg<D, 1>::kCtas : Cfg<D, 2>::kCtas);
+}
+
+// Clusters (the CTAs of one, 0: none) or runs.  With clusters, each choice of
+// CTAs costs the rounds that the GPU needs for all of them times the blocks a
+// warp then reads, plus what a CTA costs beside its blocks.  Where all row tiles
+// together have more than kMostInClusters blocks for each warp that the GPU
+// holds, runs are at least as fast and even out unequal lengths: at 1.4 blocks a
+// warp clusters take 7.9 us and runs 11.3 (144 row tiles of 16 blocks), at 7.4
+// both 22.5 (200 of 64), at 55 clusters 98 and runs 87 (192 of up to 512).
+constexpr int kMostInClusters = 8;
+struct Shares {
+    int cluster, runs;
+};
+Shares shares_for(long long tiles, int D, int nt, int blocks) {
+    const long long room = D == 32 ? ctas_of<32>(nt) : D == 64 ? ctas_of<64>(nt) : ctas_of<128>(nt);
+    if (tiles * (blocks + 1) > kMostInClusters * room * kWarps && tiles * (blocks + kPad + kOpen) < (1ll << 31))
+        return Shares{0, (int)room};
+    int best = 1;
+    long long least = 0;
+    for (int n = 1; n <= kMaxCluster; ++n) {
+        if (n > 1 && (long long)(n - 1) * kWarps > blocks) break;  // warps without a block
+        const long long rounds = (tiles * n + room - 1) / room;
+        const long long cost = rounds * ((blocks + (long long)n * kWarps - 1) / ((long long)n * kWarps) + kPerCta);
+        if (n == 1 || cost < least) {
+            least = cost;
+            best = n;
+        }
+    }
+    return Shares{best, 0};
 }
 
 struct Plan {
-    int rows, nt, tiles, splits;
+    int rows, nt, tiles;
+    Shares shares;
+    bool weigh;
     long long groups;  // row groups x row tiles
-    size_t o, ml, lb, total;
+    size_t o, ml, total, lb, bytes;  // places in the workspace, and its size
 };
-Plan make_plan(const Q8Cache &c, int H, int Tq, int list_n, bool lists, bool weight) {
+Plan make_plan(const Q8Cache &c, int H, int Tq, int list_n, bool weight) {
+    const bool lists = list_n > 0;
     Plan p;
     const int G = H / c.H;
     p.rows = lists ? G : G * Tq;
     p.nt = p.rows > 8 ? 2 : 1;
     p.tiles = (p.rows + 8 * p.nt - 1) / (8 * p.nt);
     p.groups = (long long)c.B * c.H * (lists ? Tq : 1) * p.tiles;
-    p.splits = splits_for(p.groups, c.D, lists ? (list_n < c.blocks ? list_n : c.blocks) : c.blocks);
+    p.shares = shares_for(p.groups, c.D, p.nt, lists && list_n < c.blocks ? list_n : c.blocks);
+    // a key head's rows in several tiles: the weights are summed by a kernel that finds their sums in the workspace
+    if (weight && p.shares.cluster && p.tiles > 1)
+        p.shares = Shares{0, kSms};
+    p.weigh = weight && p.shares.cluster;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    const size_t rows = (size_t)p.groups * p.splits * 8 * p.nt;
+    const size_t rows = p.shares.cluster ? 0 : (size_t)(p.groups + p.shares.runs) * 8 * p.nt;
     p.o = 0;
     p.ml = up(rows * c.D * sizeof(float));
-    p.lb = p.ml + up(rows * sizeof(float2));
-    p.total = p.lb + (weight ? up((size_t)c.B * c.H * p.rows * c.blocks * sizeof(float)) : 0);
+    p.total = p.ml + up(rows * sizeof(float2));
+    p.lb = p.total + (weight && rows ? up((size_t)p.groups * 8 * p.nt * sizeof(float)) : 0);
+    p.bytes = p.lb + (weight ? up((size_t)c.B * c.H * p.rows * c.blocks * sizeof(float)) : 0);
     return p;
 }
 
@@ -715,24 +1028,44 @@ cudaError_t launch(const DecodeArgs &a, const Plan &p, cudaStream_t st, LaunchIn
     int dev = 0;
     cudaError_t e;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    const size_t smem = sizeof(Smem<D, NT>) + 128;
+    // CTAs fill one SM after another, so a grid that leaves room asks for as much shared memory as keeps it spread out.
+    const size_t smem_most = 227 * 1024;
     static std::atomic<unsigned long long> smem_set{0};
-    if ((e = set_max_smem_once(reinterpret_cast<const void *>(decode_kernel<D, NT>), smem, dev, smem_set)) !=
+    if ((e = set_max_smem_once(reinterpret_cast<const void *>(decode_kernel<D, NT>), smem_most, dev, smem_set)) !=
         cudaSuccess)
         return e;
-    const long long grid = p.groups * p.splits;
+    const long long grid = a.cluster ? p.groups * a.cluster : a.runs;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    size_t smem = sizeof(Smem<D, NT>) + 128;
+    const long long on_sm = (grid + kSms - 1) / kSms;
+    if (on_sm < Cfg<D, NT>::kCtas) smem = smem_most / (size_t)on_sm / 1024 * 1024 - 1024;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)a.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
     if ((e = mark_main_start(li, st)) != cudaSuccess) return e;
-    if ((e = launch_pdl(decode_kernel<D, NT>, dim3((unsigned)grid), dim3(32 * Cfg<D>::kWarps), smem, st, a)) !=
-        cudaSuccess)
-        return e;
+    if ((e = cudaLaunchKernelEx(&cfg, decode_kernel<D, NT>, a)) != cudaSuccess) return e;
+    li.kernels += 1;
     if ((e = mark_main_end(li, st)) != cudaSuccess) return e;
-    if ((e = launch_pdl(join_kernel<D, NT>, dim3((unsigned)p.groups), dim3(kJoinThreads), 0, st, a)) != cudaSuccess)
-        return e;
-    li.kernels += 2;
-    if (a.weight) {
+    if (!a.cluster) {
+        if ((e = launch_pdl(join_kernel<D, NT>, dim3((unsigned)p.groups, (unsigned)(a.rows < 8 * NT ? a.rows : 8 * NT)),
+                            dim3(kJoinThreads), 0, st, a)) != cudaSuccess)
+            return e;
+        li.kernels += 1;
+    }
+    if (a.weight && !a.weigh) {
         const dim3 g((unsigned)(a.c.B * a.c.H), (unsigned)((a.c.blocks + kJoinThreads - 1) / kJoinThreads));
-        if ((e = launch_pdl(weight_kernel<NT>, g, dim3(kJoinThreads), a.rows * sizeof(float), st, a)) != cudaSuccess)
+        if ((e = launch_pdl(weight_kernel<NT>, g, dim3(kJoinThreads), 0, st, a)) != cudaSuccess)
             return e;
         li.kernels += 1;
     }
@@ -742,12 +1075,11 @@ cudaError_t launch(const DecodeArgs &a, const Plan &p, cudaStream_t st, LaunchIn
 }  // namespace
 
 size_t q8_decode_workspace(const Q8Cache &c, int H, int Tq, int list_n, bool weight) {
-    return make_plan(c, H, Tq, list_n, list_n > 0, weight).total;
+    return make_plan(c, H, Tq, list_n, weight).bytes;
 }
 
 cudaError_t q8_decode(const Q8Cache &c, const Q8Decode &d, int *err, cudaStream_t st, LaunchInfo &li) {
-    const bool lists = d.list != nullptr;
-    const Plan p = make_plan(c, d.H, d.Tq, d.list_n, lists, d.weight != 0);
+    const Plan p = make_plan(c, d.H, d.Tq, d.list_n, d.weight != 0);
     DecodeArgs a;
     a.c = c;
     a.q = d.q;
@@ -763,12 +1095,15 @@ cudaError_t q8_decode(const Q8Cache &c, const Q8Decode &d, int *err, cudaStream_
     a.Tq = d.Tq;
     a.rows = p.rows;
     a.tiles = p.tiles;
-    a.splits = p.splits;
+    a.cluster = p.shares.cluster;
+    a.runs = p.shares.runs;
+    a.weigh = p.weigh;
     a.qscale = d.scale * kLog2e;
     a.weight = d.weight;
     char *ws = static_cast<char *>(d.workspace);
     a.part.o = reinterpret_cast<float *>(ws + p.o);
     a.part.ml = reinterpret_cast<float2 *>(ws + p.ml);
+    a.part.total = reinterpret_cast<float *>(ws + p.total);
     a.part.lb = reinterpret_cast<float *>(ws + p.lb);
     a.err = err;
 #define ATTN_Q8_CASE(DD, NN) \

@@ -4,8 +4,10 @@
 //
 // Both come down to the n largest of up to 32768 numbers a head, ties to the
 // lowest index, listed in ascending order: one CTA a list holds the numbers'
-// order keys in shared memory and finds the n-th largest by its bytes, from
-// the highest one (a histogram of the keys that agree so far).
+// order keys in shared memory and finds the n-th largest eight bits at a time,
+// from the highest bit in which any two keys differ (a histogram of the keys
+// that agree so far; starting at the top byte, which scores of one size share,
+// every key would count in one bin).
 //
 // The score of block J for query q is a bound on its keys' products with q,
 // with q in 8 bits too: c = rint(127 q / max|q|),
@@ -14,8 +16,11 @@
 // with the smallest and largest key code of each channel, and the largest
 // score over the heads of a group.  It reads 2 D bytes a block, 1/64 of it;
 // the positive c take `hi` and the negative ones `lo`, so that it is two
-// four-way byte products for four channels.
+// four-way byte products for four channels.  The CTAs of a cluster share a
+// list's blocks and write their scores into the first one's shared memory.
 #include "q8_cache.cuh"
+
+#include <cooperative_groups.h>
 
 namespace attn {
 namespace {
@@ -23,99 +28,133 @@ namespace {
 using namespace sm100;
 using namespace q8;
 
-constexpr int kThreads = 256;
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
 
 struct SelectSmem {
     uint32_t hist[256];
-    uint32_t warp_sum[kWarps];
-    uint32_t bin, above;
-    uint32_t above_n[kWarps], equal_n[kWarps];
+    uint32_t low[kWarps], high[kWarps], sum[kWarps], ties[kWarps];
+    uint32_t bin, above, in_bin;
 };
+
+// Sum of x over the threads before this one, with `total` over all.
+__device__ __forceinline__ uint32_t sum_before(uint32_t x, uint32_t *of_warp, uint32_t &total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t upto = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += y;
+    }
+    if (lane == 31) of_warp[warp] = upto;
+    __syncthreads();
+    uint32_t before = upto - x;
+    total = 0;
+#pragma unroll
+    for (int y = 0; y < kWarps; ++y) {
+        if (y < warp) before += of_warp[y];
+        total += of_warp[y];
+    }
+    return before;
+}
 
 // Writes the places of the n largest of key[0 .. count - 1] to list, ascending,
 // and -1 behind them up to n.  The whole CTA calls it; keys are complete.
 __device__ void largest(const uint32_t *key, int count, int n, int32_t *list, SelectSmem &sm) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    uint32_t least = 0, ties = 0xffffffffu;  // keys above `least` are in, and the first `ties` that equal it
-    if (count > n) {
-        uint32_t prefix = 0, want = (uint32_t)n;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            sm.hist[tid] = 0;
-            __syncthreads();
-            const uint32_t high = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-            for (int i = tid; i < count; i += kThreads) {
-                const uint32_t x = key[i];
-                if ((x & high) == prefix) atomicAdd(&sm.hist[(x >> shift) & 255u], 1u);
-            }
-            __syncthreads();
-            // bin 255 - tid, summed from the highest bin down
-            const uint32_t mine = sm.hist[255 - tid];
-            uint32_t sum = mine;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const uint32_t o = __shfl_up_sync(0xffffffffu, sum, off);
-                if (lane >= off) sum += o;
-            }
-            if (lane == 31) sm.warp_sum[warp] = sum;
-            __syncthreads();
-            for (int y = 0; y < warp; ++y) sum += sm.warp_sum[y];
-            if (sum >= want && sum - mine < want) {
-                sm.bin = (uint32_t)(255 - tid);
-                sm.above = sum - mine;
-            }
-            __syncthreads();
-            prefix |= sm.bin << shift;
-            want -= sm.above;
-        }
-        least = prefix;
-        ties = want;
+    if (count <= n) {
+        for (int i = tid; i < n; i += kThreads) list[i] = i < count ? i : -1;
+        return;
     }
-    // ---- the list, kThreads keys at a time
-    uint32_t out = 0, equal_seen = 0;
-    for (int base = 0; base < count; base += kThreads) {
-        const int i = base + tid;
-        const uint32_t x = i < count ? key[i] : 0u;
-        const bool all = count <= n;
-        const bool above = i < count && (all || x > least), equal = i < count && !all && x == least;
-        const uint32_t am = __ballot_sync(0xffffffffu, above), em = __ballot_sync(0xffffffffu, equal);
+    // ---- the bits in which keys differ
+    uint32_t low = 0xffffffffu, high = 0;
+    for (int i = tid; i < count; i += kThreads) {
+        low = min(low, key[i]);
+        high = max(high, key[i]);
+    }
+    low = __reduce_min_sync(0xffffffffu, low);
+    high = __reduce_max_sync(0xffffffffu, high);
+    if (lane == 0) {
+        sm.low[warp] = low;
+        sm.high[warp] = high;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int y = 0; y < kWarps; ++y) {
+        low = min(low, sm.low[y]);
+        high = max(high, sm.high[y]);
+    }
+    int bits = 32 - __clz(low ^ high);  // bits not yet known of the n-th largest key
+    uint32_t prefix = bits == 32 ? 0u : high >> bits << bits, want = (uint32_t)n;
+    while (bits > 0) {
+        const int shift = max(0, bits - 8);
+        const uint32_t known = bits == 32 ? 0u : 0xffffffffu << bits;
+        if (tid < 256) sm.hist[tid] = 0;
         __syncthreads();
-        if (lane == 0) {
-            sm.above_n[warp] = __popc(am);
-            sm.equal_n[warp] = __popc(em);
+        for (int i = tid; i < count; i += kThreads) {
+            const uint32_t x = key[i];
+            if ((x & known) == prefix) atomicAdd(&sm.hist[(x & ~known) >> shift], 1u);
         }
         __syncthreads();
-        uint32_t a = 0, e = 0, a_all = 0, e_all = 0;
-#pragma unroll
-        for (int y = 0; y < kWarps; ++y) {
-            if (y < warp) a += sm.above_n[y], e += sm.equal_n[y];
-            a_all += sm.above_n[y], e_all += sm.equal_n[y];
+        // thread t holds bin 255 - t, so that sums run from the highest bin down
+        const uint32_t mine = tid < 256 ? sm.hist[255 - tid] : 0u;
+        uint32_t total;
+        const uint32_t above = sum_before(mine, sm.sum, total);
+        if (above < want && above + mine >= want) {
+            sm.bin = (uint32_t)(255 - tid);
+            sm.above = above;
+            sm.in_bin = mine;
         }
-        const uint32_t below = (1u << lane) - 1u;
-        a += __popc(am & below);
-        e += equal_seen + __popc(em & below);  // equal keys before this one
-        const uint32_t taken = min(e, ties) - min(equal_seen, ties);  // of those, in this round, that are in
-        if (above || (equal && e < ties)) list[out + a + taken] = i;
-        out += a_all + (min(equal_seen + e_all, ties) - min(equal_seen, ties));
-        equal_seen += e_all;
+        __syncthreads();
+        prefix |= sm.bin << shift;
+        want -= sm.above;
+        bits = shift;
+        if (sm.in_bin == want) break;  // all of the bin is in
     }
-    for (int i = (int)out + tid; i < n; i += kThreads) list[i] = -1;
+    // keys from `prefix + 2^bits` on are in, and the first `want` of those from `prefix` on (all of them, where bits > 0)
+    const uint32_t span = (1u << bits) - 1u;
+    // ---- the list: a thread takes consecutive keys
+    const int per = (count + kThreads - 1) / kThreads, i0 = min(count, tid * per), i1 = min(count, i0 + per);
+    uint32_t above = 0, equal = 0, all;
+    for (int i = i0; i < i1; ++i) {
+        const uint32_t x = key[i];
+        if (x >= prefix) {
+            if (x - prefix <= span)
+                ++equal;
+            else
+                ++above;
+        }
+    }
+    const uint32_t above_before = sum_before(above, sm.sum, all), equal_before = sum_before(equal, sm.ties, all);
+    uint32_t out = above_before + min(equal_before, want), seen = equal_before;
+    for (int i = i0; i < i1; ++i) {
+        const uint32_t x = key[i];
+        if (x >= prefix && (x - prefix > span || seen++ < want)) list[out++] = i;
+    }
 }
 
-// ---- by score.  One CTA a key head and new token.
+// ---- by score.  One cluster a key head and new token.
 template <int D>
 __global__ void __launch_bounds__(kThreads)
     select_kernel(const Q8Cache c, const __nv_bfloat16 *__restrict__ q, const TStrides sq,
-                  const int32_t *__restrict__ lens, int32_t *__restrict__ lists, int n, int G, int Tq, int *err) {
+                  const int32_t *__restrict__ lens, int32_t *__restrict__ lists, int n, int G, int Tq, int ctas,
+                  int *err) {
+    constexpr int kLanes = D / 16;       // lanes of a block, 16 channels each
+    constexpr int kAtOnce = 4;           // blocks a lane loads before it computes
     __shared__ SelectSmem sm;
-    extern __shared__ uint32_t dyn[];
-    uint32_t *key = dyn;                                            // [blocks]
-    uint32_t *pos = dyn + (c.blocks + 3) / 4 * 4;                   // [G][D / 4] codes above zero
-    uint32_t *neg = pos + G * (D / 4);                              // [G][D / 4] codes below zero
-    float *qs = reinterpret_cast<float *>(neg + G * (D / 4));       // [G] max|q| / 127
+    extern __shared__ uint4 dyn[];
+    uint4 *pos = dyn;                                               // [G][D / 16] codes above zero
+    uint4 *neg = pos + G * kLanes;                                  // [G][D / 16] codes below zero
+    float *qs = reinterpret_cast<float *>(neg + G * kLanes);        // [G] max|q| / 127
+    uint32_t *key = reinterpret_cast<uint32_t *>(qs + G);           // [blocks]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int r = (int)(blockIdx.x % Tq);
-    const long long bh = blockIdx.x / Tq;
+    const unsigned which = blockIdx.x / ctas;
+    const int rank = (int)(blockIdx.x - which * ctas);
+    const int r = (int)(which % Tq);
+    const long long bh = which / Tq;
     const int b = (int)(bh / c.H), h = (int)(bh % c.H);
     grid_dep_wait();
     grid_dep_launch();
@@ -123,8 +162,7 @@ __global__ void __launch_bounds__(kThreads)
     if (L < 0) L = 0;
     const int last = L - Tq + r;  // the query's own position
     const int count = last < 0 ? 0 : min(L / kBlock, last / kBlock + 1);
-    int32_t *list = lists + ((long long)blockIdx.x) * n;
-    if (count > n) {
+    if (count > n) {  // (the same in all CTAs of the cluster)
         // ---- the queries' codes, a warp a head, four channels a lane
         for (int x = warp; x < G; x += kWarps) {
             uint2 w = make_uint2(0, 0);
@@ -134,60 +172,78 @@ __global__ void __launch_bounds__(kThreads)
             uint32_t m = __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
             m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
             const float most = __uint_as_float(m << 16);
-            const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w.x));
-            const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w.y));
-            const float f[4] = {f0.x, f0.y, f1.x, f1.y};
             uint32_t p = 0, ng = 0;
             if (m != 0 && m < 0x7f80u) {
+                const uint32_t codes = Coder(most)(w.x, w.y);
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const int code = code_number(f[y], most);
+                    const int code = (int)((codes >> (8 * y)) & 255u) - 128;
                     p |= (uint32_t)(max(code, 0) & 255) << (8 * y);
                     ng |= (uint32_t)(min(code, 0) & 255) << (8 * y);
                 }
             }
             if (lane < D / 4) {
-                pos[x * (D / 4) + lane] = p;
-                neg[x * (D / 4) + lane] = ng;
+                reinterpret_cast<uint32_t *>(pos)[x * (D / 4) + lane] = p;
+                reinterpret_cast<uint32_t *>(neg)[x * (D / 4) + lane] = ng;
             }
             if (lane == 0) qs[x] = __fdiv_rn(most, 127.f);  // an infinity or a NaN stays one
         }
         __syncthreads();
-        // ---- the scores: D / 16 lanes a block, 16 channels each
-        constexpr int kLanes = D / 16;
+        // ---- the scores
+        uint32_t *to = ctas > 1 ? cg::this_cluster().map_shared_rank(key, 0) : key;
         const int part = tid % kLanes;
-        for (int j0 = 0; j0 < count; j0 += kThreads / kLanes) {
-            const int j = j0 + tid / kLanes;
-            uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-            float ks = 0.f;
-            if (j < count) {
-                const long long at = bh * c.blocks + j;
-                const uint4 *e = reinterpret_cast<const uint4 *>(c.bounds + at * (2 * D));
-                lo = e[part];
-                hi = e[kLanes + part];
-                ks = c.scales[2 * at];
-            }
-            const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
-            float best = -INFINITY;
-            bool none = false;
-            for (int x = 0; x < G; ++x) {
-                int dot = 0;
+        constexpr int kRow = kThreads / kLanes;  // blocks of a step
+        for (int j0 = rank * kRow * kAtOnce; j0 < count; j0 += ctas * kRow * kAtOnce) {
+            uint4 lo[kAtOnce], hi[kAtOnce];
+            float ks[kAtOnce];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    dot = __dp4a((int)pos[x * (D / 4) + 4 * part + y], (int)hw[y], dot);
-                    dot = __dp4a((int)neg[x * (D / 4) + 4 * part + y], (int)lw[y], dot);
+            for (int y = 0; y < kAtOnce; ++y) {
+                const int j = j0 + y * kRow + tid / kLanes;
+                lo[y] = hi[y] = make_uint4(0, 0, 0, 0);
+                ks[y] = 0.f;
+                if (j < count) {
+                    const long long at = bh * c.blocks + j;
+                    const uint4 *e = reinterpret_cast<const uint4 *>(c.bounds + at * (2 * D));
+                    lo[y] = e[part];
+                    hi[y] = e[kLanes + part];
+                    ks[y] = c.scales[2 * at];
                 }
-#pragma unroll
-                for (int off = 1; off < kLanes; off <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-                const float score = __fmul_rn(__fmul_rn((float)dot, ks), qs[x]);
-                none = none || score != score;
-                best = fmaxf(best, score);
             }
-            if (part == 0 && j < count) key[j] = none ? kFirst - 1 : order_key(best);
+            float best[kAtOnce];
+            bool none[kAtOnce];
+#pragma unroll
+            for (int y = 0; y < kAtOnce; ++y) {
+                best[y] = -INFINITY;
+                none[y] = false;
+            }
+            for (int x = 0; x < G; ++x) {
+                const uint4 p = pos[x * kLanes + part], m = neg[x * kLanes + part];
+                const float scale = qs[x];
+#pragma unroll
+                for (int y = 0; y < kAtOnce; ++y) {
+                    int dot = __dp4a((int)p.x, (int)hi[y].x, __dp4a((int)m.x, (int)lo[y].x, 0));
+                    dot = __dp4a((int)p.y, (int)hi[y].y, __dp4a((int)m.y, (int)lo[y].y, dot));
+                    dot = __dp4a((int)p.z, (int)hi[y].z, __dp4a((int)m.z, (int)lo[y].z, dot));
+                    dot = __dp4a((int)p.w, (int)hi[y].w, __dp4a((int)m.w, (int)lo[y].w, dot));
+#pragma unroll
+                    for (int off = 1; off < kLanes; off <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+                    const float score = __fmul_rn(__fmul_rn((float)dot, ks[y]), scale);
+                    none[y] = none[y] || score != score;
+                    best[y] = fmaxf(best[y], score);
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < kAtOnce; ++y) {
+                const int j = j0 + y * kRow + tid / kLanes;
+                if (part == 0 && j < count) to[j] = none[y] ? kFirst - 1 : order_key(best[y]);
+            }
         }
-        __syncthreads();
+        if (ctas > 1)
+            cg::this_cluster().sync();
+        else
+            __syncthreads();
     }
-    largest(key, count, n, list, sm);
+    if (rank == 0) largest(key, count, n, lists + (long long)which * n, sm);
 }
 
 // ---- by weight.  One CTA a key head; `state` takes twice the count of kept
@@ -225,11 +281,12 @@ __global__ void __launch_bounds__(kThreads)
 // cache: a block's new place is never behind its old one.  The CTA of the last
 // slice moves everything else.
 constexpr int kSlice = 1024;
-constexpr int kAtOnce = kThreads / (kSlice / 16);  // blocks whose slices a CTA moves side by side
+constexpr int kMoveThreads = 256;
+constexpr int kAtOnce = kMoveThreads / (kSlice / 16);  // blocks whose slices a CTA moves side by side
 constexpr int kRounds = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kMoveThreads)
     move_kernel(const Q8Cache c, const Q8Cache d, const int32_t *__restrict__ lens, int32_t *__restrict__ lens_out,
                 const int32_t *__restrict__ kept, int keep, const int *__restrict__ state, int chunks, int *err) {
     constexpr int kBytes = kBlock * D;            // codes of a block's keys
@@ -273,7 +330,7 @@ __global__ void __launch_bounds__(kThreads)
         return;
     }
     // ---- scales, bounds and weight
-    for (int i0 = begin; i0 < end; i0 += kThreads) {
+    for (int i0 = begin; i0 < end; i0 += kMoveThreads) {
         const int i = i0 + tid;
         float2 s = make_float2(0.f, 0.f);
         float w = 0.f;
@@ -290,7 +347,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (d.bounds) {
         constexpr int kWords = 2 * D / 16;  // 16-byte words of a block's bounds
-        for (int e0 = begin * kWords; e0 < end * kWords; e0 += kThreads) {
+        for (int e0 = begin * kWords; e0 < end * kWords; e0 += kMoveThreads) {
             const int e = e0 + tid, i = e / kWords;
             uint4 x = make_uint4(0, 0, 0, 0);
             if (e < end * kWords)
@@ -311,7 +368,7 @@ __global__ void __launch_bounds__(kThreads)
     const uint4 *sv = reinterpret_cast<const uint4 *>(c.recent_v) + bh * 2 * kChunks;
     uint4 *dk = reinterpret_cast<uint4 *>(d.recent_k) + bh * 2 * kChunks;
     uint4 *dv = reinterpret_cast<uint4 *>(d.recent_v) + bh * 2 * kChunks;
-    for (int e = tid; e < kChunks; e += kThreads) {  // a thread alone reads and writes both halves' chunk e
+    for (int e = tid; e < kChunks; e += kMoveThreads) {  // a thread alone reads and writes both halves' chunk e
         const uint4 k0 = sk[e], k1 = sk[kChunks + e], v0 = sv[e], v1 = sv[kChunks + e];
         dk[other + e] = k0;
         dk[kChunks - other + e] = k1;
@@ -327,7 +384,13 @@ cudaError_t q8_select(const Q8Cache &c, const __nv_bfloat16 *q, const TStrides &
     const int G = H / c.H;
     const long long grid = (long long)c.B * c.H * Tq;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const size_t smem = ((size_t)(c.blocks + 3) / 4 * 4 + 2 * (size_t)G * (c.D / 4) + G) * 4;
+    const size_t smem = ((size_t)c.blocks + 2 * (size_t)G * (c.D / 4) + G) * 4;
+    // CTAs of a cluster: a step of 512 threads takes 16 D^-1 * 512 * 4 blocks; as many as there are steps, while the
+    // GPU's 148 SMs have room for two CTAs each.
+    const int step = kThreads / (c.D / 16) * 4;
+    int ctas = (int)(2 * 148 / grid);
+    ctas = ctas > kMaxCluster ? kMaxCluster : ctas < 1 ? 1 : ctas;
+    if (ctas > (c.blocks + step - 1) / step) ctas = (c.blocks + step - 1) / step;
     const void *fn = c.D == 32 ? (const void *)select_kernel<32>
                                : c.D == 64 ? (const void *)select_kernel<64> : (const void *)select_kernel<128>;
     int dev = 0;
@@ -337,13 +400,26 @@ cudaError_t q8_select(const Q8Cache &c, const __nv_bfloat16 *q, const TStrides &
     const size_t most = ((size_t)kQ8MaxBlocks + 2 * kQ8MaxGroup * (128 / 4) + kQ8MaxGroup) * 4;
     if ((e = set_max_smem_once(fn, most, dev, smem_set[c.D == 32 ? 0 : c.D == 64 ? 1 : 2])) != cudaSuccess) return e;
     if ((e = mark_main_start(li, st)) != cudaSuccess) return e;
-    const dim3 g((unsigned)grid), t(kThreads);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(grid * ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
     if (c.D == 32)
-        e = launch_pdl(select_kernel<32>, g, t, smem, st, c, q, sq, lens, list, list_n, G, Tq, err);
+        e = cudaLaunchKernelEx(&cfg, select_kernel<32>, c, q, sq, lens, list, list_n, G, Tq, ctas, err);
     else if (c.D == 64)
-        e = launch_pdl(select_kernel<64>, g, t, smem, st, c, q, sq, lens, list, list_n, G, Tq, err);
+        e = cudaLaunchKernelEx(&cfg, select_kernel<64>, c, q, sq, lens, list, list_n, G, Tq, ctas, err);
     else
-        e = launch_pdl(select_kernel<128>, g, t, smem, st, c, q, sq, lens, list, list_n, G, Tq, err);
+        e = cudaLaunchKernelEx(&cfg, select_kernel<128>, c, q, sq, lens, list, list_n, G, Tq, ctas, err);
     if (e != cudaSuccess) return e;
     li.kernels += 1;
     return mark_main_end(li, st);
@@ -369,7 +445,7 @@ cudaError_t q8_evict(const Q8Cache &src, const Q8Cache &dst, const int32_t *lens
                         keep, sink, recent, workspace, err)) != cudaSuccess)
         return e;
     if ((e = mark_main_start(li, st)) != cudaSuccess) return e;
-    const dim3 g((unsigned)grid), t(kThreads);
+    const dim3 g((unsigned)grid), t(kMoveThreads);
     if (src.D == 32)
         e = launch_pdl(move_kernel<32>, g, t, 0, st, src, dst, lens, lens_out, kept, keep, workspace, chunks, err);
     else if (src.D == 64)

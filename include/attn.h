@@ -365,7 +365,8 @@ typedef struct {
 } attn_q8_decode_options;
 
 /* Bytes of device workspace attn_q8_decode needs for a cache of these sizes
- * (its pointers are not looked at) and these options; 0 on a bad shape. */
+ * (its pointers are not looked at) and these options; 0 where it needs none
+ * (most calls that keep no weights), and on a bad shape. */
 size_t attn_q8_decode_workspace_bytes(const attn_q8_cache *cache, int H, int Tq,
                                       const attn_q8_decode_options *opts);
 
@@ -377,8 +378,9 @@ size_t attn_q8_decode_workspace_bytes(const attn_q8_cache *cache, int H, int Tq,
  * one).  1 <= Tq <= ATTN_DECODE_MAX_QUERIES.  Query r is the token at position
  * lens[b] - Tq + r; where that is below zero nothing is seen: o = 0, lse =
  * -inf.  workspace: at least attn_q8_decode_workspace_bytes bytes, 256-byte
- * aligned, its contents do not matter.  Two launches, a third one with
- * weights. */
+ * aligned, its contents do not matter (NULL where that is 0).  One launch;
+ * one more to join the parts of few heads over many blocks, and one for the
+ * weights of such heads and of more than 16 rows. */
 int attn_q8_decode(const attn_q8_cache *cache, const void *q, void *o, float *lse,
                    const int32_t *lens, int H, int Tq, float scale, const attn_strides *strides,
                    const attn_q8_decode_options *opts, void *workspace, size_t workspace_bytes,
