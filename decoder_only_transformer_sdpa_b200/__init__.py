@@ -551,7 +551,7 @@ class Q8Cache:
     Sequence lengths are the caller's: an int32 CUDA tensor ``lens`` [B] that
     counts the new tokens before they are appended."""
     __slots__ = ("k_codes", "v_codes", "scales", "bounds", "weight", "recent_k", "recent_v", "B", "H",
-                 "blocks", "D", "device", "index", "struct", "ref", "needs")
+                 "blocks", "D", "device", "index", "struct", "ref", "needs", "batch", "types")
 
     def __init__(self, k_codes, v_codes, scales, bounds, weight, recent_k, recent_v):
         torch = _torch()
@@ -578,6 +578,7 @@ class Q8Cache:
         self.ref = ctypes.byref(self.struct)
         self.index = self.device.index
         self.needs = {}  # workspace bytes by (query heads, new tokens, list length, weights)
+        self.batch, self.types = (B,), (torch.bfloat16, torch.int32, torch.float32)
 
     @classmethod
     def empty(cls, B: int, H: int, D: int, max_tokens: int, device="cuda", bounds: bool = True,
@@ -616,11 +617,10 @@ def _whole(t, name, dtype, shape, index):
     return p
 
 
-def _view(t, name, shape, index):
+def _view(t, name, dtype, shape, index):
     """The same for a bf16 [B, H, T, D] view with unit stride along D."""
     try:
-        if (t.get_device() == index and t.dtype is _torch().bfloat16 and t.shape == shape
-                and t.stride(3) == 1):
+        if t.get_device() == index and t.dtype is dtype and t.shape == shape and t.stride(3) == 1:
             return t.data_ptr()
     except AttributeError:
         pass
@@ -632,19 +632,18 @@ def _view(t, name, shape, index):
 def _used_on(stream, index, *tensors):
     """Tells the allocator that tensors made for this call are in use on a
     stream other than the current one."""
-    if stream is not None and stream != _torch().cuda.current_stream(index):
+    if stream != _torch().cuda.current_stream(index):
         for t in tensors:
             t.record_stream(stream)
 
 
 def _call(fn, where, index, stream, *args):
     """The library call on device `index`, on `stream` (None: the current one of that device)."""
-    torch = _torch()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None and torch.cuda.current_device() == index:
-        status = fn(*args, raw(index) if stream is None else stream.cuda_stream)
+    C = _torch()._C
+    if stream is None and C._cuda_getDevice() == index:
+        status = fn(*args, C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(index):
+        with _torch().cuda.device(index):
             status = fn(*args, _stream_handle(stream))
     if status != 0:
         raise AttnError(status, where)
@@ -655,13 +654,13 @@ def attn_q8_append(cache, k, v, lens, new_lens=None, stream=None) -> None:
     or strided views) into the cache.  ``lens`` [B] int32 counts them already;
     ``new_lens`` [B] int32: how many of the n rows are sequence b's (the first
     ones; None: all n)."""
-    i32 = _torch().int32
     index = _check_cache(cache)
+    bf16, i32, _ = cache.types
     n = _shape4(k)[2]
     shape = (cache.B, cache.H, n, cache.D)
-    kp, vp = _view(k, "k", shape, index), _view(v, "v", shape, index)
-    lp = _whole(lens, "lens", i32, (cache.B,), index)
-    np_ = None if new_lens is None else _whole(new_lens, "new_lens", i32, (cache.B,), index)
+    kp, vp = _view(k, "k", bf16, shape, index), _view(v, "v", bf16, shape, index)
+    lp = _whole(lens, "lens", i32, cache.batch, index)
+    np_ = None if new_lens is None else _whole(new_lens, "new_lens", i32, cache.batch, index)
     st = None if k.is_contiguous() and v.is_contiguous() else _strides_of(k, v)
     _call(_lib.attn_q8_append, "attn_q8_append", index, stream, cache.ref, kp, vp, n, lp, np_, st)
 
@@ -669,19 +668,27 @@ def attn_q8_append(cache, k, v, lens, new_lens=None, stream=None) -> None:
 def attn_q8_read(cache, lens, n: int, starts=None, k=None, v=None, stream=None):
     """Positions starts[b] .. + n - 1 (None: from 0) as the cache holds them,
     in bf16 [B, H, n, D], zero past a sequence's end.  Returns (k, v)."""
-    torch = _torch()
     index = _check_cache(cache)
+    bf16, i32, _ = cache.types
     shape = (cache.B, cache.H, int(n), cache.D)
+    if n < 1:
+        raise AttnError(-2, "attn_q8_read")
+    lp = _whole(lens, "lens", i32, cache.batch, index)
+    sp = None if starts is None else _whole(starts, "starts", i32, cache.batch, index)
     made = []
     if k is None:
         made.append(k := cache.recent_k.new_empty(shape))
+        kp = k.data_ptr()
+    else:
+        kp = _whole(k, "k", bf16, shape, index)
     if v is None:
         made.append(v := cache.recent_k.new_empty(shape))
-    lp = _whole(lens, "lens", torch.int32, (cache.B,), index)
-    sp = None if starts is None else _whole(starts, "starts", torch.int32, (cache.B,), index)
-    kp, vp = (_whole(t, name, torch.bfloat16, shape, index) for t, name in ((k, "k"), (v, "v")))
+        vp = v.data_ptr()
+    else:
+        vp = _whole(v, "v", bf16, shape, index)
     _call(_lib.attn_q8_read, "attn_q8_read", index, stream, cache.ref, lp, sp, int(n), kp, vp)
-    _used_on(stream, index, *made)
+    if stream is not None:
+        _used_on(stream, index, *made)
     return k, v
 
 
@@ -701,29 +708,33 @@ def attn_q8_decode(q, cache, lens, o=None, lse=None, scale: Optional[float] = No
     blocks to attend to (the open one always is).  ``weight``: "set" or "add"
     to keep the attention weight of each closed block in cache.weight.
     Returns (O [B, Hq, Tq, D], lse [B, Hq, Tq])."""
-    torch = _torch()
     index = _check_cache(cache)
+    bf16, i32, f32 = cache.types
     _, H, Tq, D = _shape4(q)
     keep = _Q8_WEIGHT.get(weight)
     if keep is None:
         raise ValueError("weight must be None, 'set' or 'add'")
     shape = (cache.B, H, Tq, cache.D)
-    qp = _view(q, "q", shape, index)
+    qp = _view(q, "q", bf16, shape, index)
+    lp = _whole(lens, "lens", i32, cache.batch, index)
     plain = q.is_contiguous()
     made = []
     if o is None:
-        made.append(o := torch.empty_like(q) if plain else q.new_empty(shape))
+        made.append(o := _torch().empty_like(q) if plain else q.new_empty(shape))
+        op = o.data_ptr()
+    else:
+        op = _view(o, "o", bf16, shape, index)
     if lse is None:
-        made.append(lse := q.new_empty(shape[:3], dtype=torch.float32))
-    op = _view(o, "o", shape, index)
-    ep = _whole(lse, "lse", torch.float32, shape[:3], index)
-    lp = _whole(lens, "lens", torch.int32, (cache.B,), index)
+        made.append(lse := q.new_empty(shape[:3], dtype=f32))
+        ep = lse.data_ptr()
+    else:
+        ep = _whole(lse, "lse", f32, shape[:3], index)
     n, opts = 0, None
     if blocks is not None:
-        if not isinstance(blocks, torch.Tensor) or blocks.dim() != 4 or blocks.shape[3] < 1:
+        if not isinstance(blocks, _torch().Tensor) or blocks.dim() != 4 or blocks.shape[3] < 1:
             raise ValueError("blocks must be a [B, H, Tq, n] tensor")
         n = blocks.shape[3]
-        opts = attn_q8_decode_options(_whole(blocks, "blocks", torch.int32, (cache.B, cache.H, Tq, n), index), n, keep)
+        opts = attn_q8_decode_options(_whole(blocks, "blocks", i32, (cache.B, cache.H, Tq, n), index), n, keep)
     elif keep:
         opts = attn_q8_decode_options(None, 0, keep)
     if workspace is None:
@@ -739,7 +750,8 @@ def attn_q8_decode(q, cache, lens, o=None, lse=None, scale: Optional[float] = No
     st = None if plain and o.is_contiguous() else _strides_of(q, o)
     _call(_lib.attn_q8_decode, "attn_q8_decode", index, stream, cache.ref, qp, op, ep, lp, H, Tq,
           1.0 / math.sqrt(D) if scale is None else float(scale), st, opts, wp, wn)
-    _used_on(stream, index, *made)
+    if stream is not None:
+        _used_on(stream, index, *made)
     return o, lse
 
 
@@ -747,21 +759,24 @@ def attn_q8_select(q, cache, lens, n: int, blocks=None, stream=None):
     """The n closed blocks that each query of q (as in attn_q8_decode) is
     likely to attend to most, by a bound on their keys' products with it:
     int32 [B, H, Tq, n], ascending, -1 behind the last."""
-    i32 = _torch().int32
     index = _check_cache(cache)
+    bf16, i32, _ = cache.types
     _, H, Tq, _ = _shape4(q)
+    if n < 1:
+        raise AttnError(-2, "attn_q8_select")
     shape = (cache.B, cache.H, Tq, int(n))
-    qp = _view(q, "q", (cache.B, H, Tq, cache.D), index)
-    lp = _whole(lens, "lens", i32, (cache.B,), index)
+    qp = _view(q, "q", bf16, (cache.B, H, Tq, cache.D), index)
+    lp = _whole(lens, "lens", i32, cache.batch, index)
     made = []
     if blocks is None:
-        if n < 1:
-            raise AttnError(-2, "attn_q8_select")
         made.append(blocks := lens.new_empty(shape))
-    bp = _whole(blocks, "blocks", i32, shape, index)
+        bp = blocks.data_ptr()
+    else:
+        bp = _whole(blocks, "blocks", i32, shape, index)
     st = None if q.is_contiguous() else _strides_of(q)
     _call(_lib.attn_q8_select, "attn_q8_select", index, stream, cache.ref, qp, lp, bp, int(n), H, Tq, st)
-    _used_on(stream, index, *made)
+    if stream is not None:
+        _used_on(stream, index, *made)
     return blocks
 
 
@@ -776,26 +791,35 @@ def attn_q8_evict(cache, lens, keep: int, sink: int = 0, recent: int = 1, out=No
     moved to the front of ``out`` (None: of the cache itself).  Returns
     (lens_out [B], kept [B, H, keep]: the places the blocks came from, -1
     behind the last)."""
-    i32 = _torch().int32
     index = _check_cache(cache)
+    i32 = cache.types[1]
     out = cache if out is None else out
     if _check_cache(out, "out") != index:
         raise ValueError(f"out must be on cuda:{index}, got {out.device}")
     if keep < 1:
         raise AttnError(-2, "attn_q8_evict")
-    lp = _whole(lens, "lens", i32, (cache.B,), index)
+    lp = _whole(lens, "lens", i32, cache.batch, index)
     made = []
     if lens_out is None:
-        made.append(lens_out := lens.new_empty((cache.B,)))
+        made.append(lens_out := lens.new_empty(cache.batch))
+        op = lens_out.data_ptr()
+    else:
+        op = _whole(lens_out, "lens_out", i32, cache.batch, index)
+    shape = (cache.B, cache.H, int(keep))
     if kept is None:
-        made.append(kept := lens.new_empty((cache.B, cache.H, int(keep))))
+        made.append(kept := lens.new_empty(shape))
+        kp = kept.data_ptr()
+    else:
+        kp = _whole(kept, "kept", i32, shape, index)
     if workspace is None:
-        made.append(workspace := cache.k_codes.new_empty(attn_q8_evict_workspace_bytes(cache)))
+        need = cache.needs.get("evict")
+        if need is None:
+            need = cache.needs["evict"] = attn_q8_evict_workspace_bytes(cache)
+        made.append(workspace := cache.k_codes.new_empty(need))
     elif not workspace.is_contiguous() or workspace.get_device() != index:
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
-    op = _whole(lens_out, "lens_out", i32, (cache.B,), index)
-    kp = _whole(kept, "kept", i32, (cache.B, cache.H, int(keep)), index)
     _call(_lib.attn_q8_evict, "attn_q8_evict", index, stream, cache.ref, out.ref, lp, op, kp, int(keep), int(sink),
           int(recent), workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _used_on(stream, index, *made)
+    if stream is not None:
+        _used_on(stream, index, *made)
     return lens_out, kept
