@@ -27,8 +27,8 @@
 //
 // How the work is shared out goes by its size alone (shares_for):
 //   * little work: the CTAs of a cluster share a row tile, each block going to
-//     the next of their warps, and the cluster's first CTA joins the results
-//     through distributed shared memory: one launch;
+//     the next of their warps, and they join their results through distributed
+//     shared memory: one launch;
 //   * much of it: as many CTAs as the GPU holds take equal runs of all blocks of
 //     all row tiles, whatever the sequences' lengths (which only the kernel
 //     knows); a second kernel joins what the runs left of each row tile.
@@ -62,6 +62,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The first product of a sum.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+        " {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
@@ -90,6 +97,8 @@ struct Cfg {
     static constexpr int kHalves = D == 128 ? 2 : 1;  // slots of a block
     static constexpr int kSlots = D == 32 ? 4 : (NT == 1 ? 2 : 3);
     static constexpr bool kQueriesInSmem = NT == 2;  // else in registers
+    // tiles of 16 tokens (keys) or 16 channels (values) whose sums a warp forms side by side
+    static constexpr int kAtOnce = D == 32 ? 2 : 4 / NT;
 };
 
 // Layout of the workspace: what each run left of a row tile (its unnormalised
@@ -309,14 +318,22 @@ __device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&s)[Tiles]
     }
 }
 
+// A load that stays where it is written, ahead of what it overlaps with.
+__device__ __forceinline__ uint4 load_now(const void *p) {
+    uint4 w;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(p));
+    return w;
+}
+
 // One bf16 row chunk of the lane: channels slab * S + (S / 4) t + 0 .. S / 4 - 1.
-template <int D>
+template <int D, bool Now = false>
 __device__ __forceinline__ void load_row(uint32_t (&w)[D / 8], const __nv_bfloat16 *row, int t) {
     constexpr int S = slab(D);
 #pragma unroll
     for (int i = 0; i < D / 8; i += 4) {  // four words = eight channels
         const int sl = i / (S / 8), in = i % (S / 8);
-        const uint4 x = *reinterpret_cast<const uint4 *>(row + sl * S + (S / 4) * t + 2 * in);
+        const __nv_bfloat16 *from = row + sl * S + (S / 4) * t + 2 * in;
+        const uint4 x = Now ? load_now(from) : *reinterpret_cast<const uint4 *>(from);
         w[i] = x.x;
         w[i + 1] = x.y;
         w[i + 2] = x.z;
@@ -457,7 +474,8 @@ __device__ __forceinline__ void write_weight(const DecodeArgs &a, long long bh, 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(const __grid_constant__ DecodeArgs a) {
     using Sm = Smem<D, NT>;
-    constexpr int SL = Sm::kSlots, kRows = Sm::kRows, S = slab(D), kHalves = Cfg<D, NT>::kHalves;
+    constexpr int SL = Sm::kSlots, kRows = Sm::kRows, S = slab(D), kHalves = Cfg<D, NT>::kHalves,
+                  kAtOnce = Cfg<D, NT>::kAtOnce;
     constexpr int kSide = kBlock * D;  // bytes of a block's keys, and of its values
     static_assert(sizeof(float) * kWarps * kRows * Sm::kPitch + sizeof(float) * kRows * D <= sizeof(Sm::ring),
                   "the outputs take no more than the rings");
@@ -491,6 +509,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
     bool ok = true;
     while (true) {
         const Where w = where(a, group);
+        // ---- queries: this lane's row g of each row tile (on their way while the lengths are)
+        uint32_t qx[NT][D / 8];
+        const __nv_bfloat16 *qrow[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = w.tile * kRows + nt * 8 + g;
+            qrow[nt] = nullptr;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) qx[nt][i] = 0;
+            if (row < a.rows) {
+                qrow[nt] = a.q + (long long)w.b * a.sq.b + (long long)(w.h * a.G + row_head(a, row)) * a.sq.h +
+                           (long long)row_token(a, w, row) * a.sq.t;
+                load_row<D, true>(qx[nt], qrow[nt], t);
+            }
+        }
         int L = checked_length(a.lens, w.b, a.c.blocks, a.err);
         if (L < 0) L = 0;
         // ---- this warp's blocks: places first, first + step, ... below `count` (of all closed blocks, or of the list),
@@ -583,23 +616,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
         int at = first, id = block_from(at);
         float2 sc = id >= 0 ? scales[id] : make_float2(0.f, 0.f);
 
-        // ---- queries: fragments of this lane's row g of each row tile, and the factors of rows 2t, 2t + 1
+        // ---- the queries as f16 fragments, and the factors of rows 2t, 2t + 1
         uint32_t qf[Cfg<D, NT>::kQueriesInSmem ? 1 : NT][D / 8];
-        const __nv_bfloat16 *qrow[NT];
         float rowf[NT][2];
         int sees[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int row = w.tile * kRows + nt * 8 + g;
-            qrow[nt] = nullptr;
-            uint32_t x[D / 8];
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) x[i] = 0;
-            if (row < a.rows) {
-                qrow[nt] = a.q + (long long)w.b * a.sq.b + (long long)(w.h * a.G + row_head(a, row)) * a.sq.h +
-                           (long long)row_token(a, w, row) * a.sq.t;
-                load_row<D>(x, qrow[nt], t);
-            }
+            uint32_t(&x)[D / 8] = qx[nt];
             uint32_t mx = 0;
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) mx = __vmaxu2(mx, x[i] & 0x7fff7fffu);
@@ -665,17 +688,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
             // further, which is the order in which a lane's 16 value bytes pair up below
             float sv[4][NT][4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) sv[u][nt][0] = sv[u][nt][1] = sv[u][nt][2] = sv[u][nt][3] = 0.f;
-#pragma unroll
             for (int sl = 0; sl < D / S; ++sl) {
                 const uint8_t *kb = sm.ring[warp][slot] + sl * (kBlock * S) + (16 * (g >> 1) + (g & 1)) * S + t * (S / 4);
 #pragma unroll
-                for (int u0 = 0; u0 < 4; u0 += 2) {  // two tiles at a time: 16 registers of codes
-                    uint32_t r0[2][S / 16], r1[2][S / 16];
+                for (int u0 = 0; u0 < 4; u0 += kAtOnce) {
+                    uint32_t r0[kAtOnce][S / 16], r1[kAtOnce][S / 16];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
+                    for (int u = 0; u < kAtOnce; ++u) {
                         const uint8_t *from = kb + 4 * (u0 + u) * S;
                         if constexpr (S == 64) {
                             const uint4 x = *reinterpret_cast<const uint4 *>(from);
@@ -691,9 +710,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
                     }
 #pragma unroll
                     for (int k = 0; k < S / 16; ++k) {
-                        uint32_t ka[2][4];
+                        uint32_t ka[kAtOnce][4];
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
+                        for (int u = 0; u < kAtOnce; ++u) {
                             ka[u][0] = codes_f16x2<0>(r0[u][k]);
                             ka[u][1] = codes_f16x2<0>(r1[u][k]);
                             ka[u][2] = codes_f16x2<1>(r0[u][k]);
@@ -703,7 +722,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
                         for (int nt = 0; nt < NT; ++nt) {
                             const uint2 q = query(nt, sl * (S / 16) + k);
 #pragma unroll
-                            for (int u = 0; u < 2; ++u) mma_f16(sv[u0 + u][nt], ka[u], q.x, q.y);
+                            for (int u = 0; u < kAtOnce; ++u) {
+                                if (sl == 0 && k == 0)
+                                    mma_f16_first(sv[u0 + u][nt], ka[u], q.x, q.y);
+                                else
+                                    mma_f16(sv[u0 + u][nt], ka[u], q.x, q.y);
+                            }
                         }
                     }
                 }
@@ -756,26 +780,37 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
             if (kHalves == 2 && !(ok = wait())) break;
             const uint8_t *vb = sm.ring[warp][slot] + (kHalves == 2 ? 0 : kSide) + g * kBlock + 16 * t;
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(vb + 16 * c * kBlock);
-                const uint4 y = *reinterpret_cast<const uint4 *>(vb + (16 * c + 8) * kBlock);
-                const uint32_t r0[4] = {x.x, x.y, x.z, x.w}, r1[4] = {y.x, y.y, y.z, y.w};
-                float acc[NT][4];
+            for (int c0 = 0; c0 < D / 16; c0 += kAtOnce) {
+                uint32_t r0[kAtOnce][4], r1[kAtOnce][4];
+                float acc[kAtOnce][NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint32_t va[4] = {codes_f16x2<0>(r0[u]), codes_f16x2<0>(r1[u]), codes_f16x2<1>(r0[u]),
-                                            codes_f16x2<1>(r1[u])};
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], va, p[u][nt][0], p[u][nt][1]);
+                for (int c = 0; c < kAtOnce; ++c) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(vb + 16 * (c0 + c) * kBlock);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(vb + (16 * (c0 + c) + 8) * kBlock);
+                    r0[c][0] = x.x, r0[c][1] = x.y, r0[c][2] = x.z, r0[c][3] = x.w;
+                    r1[c][0] = y.x, r1[c][1] = y.y, r1[c][2] = y.z, r1[c][3] = y.w;
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int u = 0; u < 4; ++u)
 #pragma unroll
-                    for (int y2 = 0; y2 < 4; ++y2) {
-                        st.o[c][nt][y2] = fmaf(sc.y, acc[nt][y2], st.o[c][nt][y2]);
+                    for (int c = 0; c < kAtOnce; ++c) {
+                        const uint32_t va[4] = {codes_f16x2<0>(r0[c][u]), codes_f16x2<0>(r1[c][u]),
+                                                codes_f16x2<1>(r0[c][u]), codes_f16x2<1>(r1[c][u])};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (u == 0)
+                                mma_f16_first(acc[c][nt], va, p[u][nt][0], p[u][nt][1]);
+                            else
+                                mma_f16(acc[c][nt], va, p[u][nt][0], p[u][nt][1]);
+                        }
                     }
+#pragma unroll
+                for (int c = 0; c < kAtOnce; ++c)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            st.o[c0 + c][nt][x] = fmaf(sc.y, acc[c][nt][x], st.o[c0 + c][nt][x]);
             }
             next();
             at = at_next;
@@ -847,13 +882,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
             __syncthreads();  // the rings take blocks again
             continue;
         }
-        // ---- the cluster's results into one, in its first CTA
+        // ---- the cluster's results into one, every CTA a part of them
         if (a.cluster > 1)
             cluster.sync();
         else
             __syncthreads();
-        if (a.cluster > 1 && rank == 0) {
-            for (int e = tid; e < here * (D / 4); e += kThreads) {
+        if (a.cluster > 1) {
+            for (int e = rank * kThreads + tid; e < here * (D / 4); e += a.cluster * kThreads) {
                 const int row = e / (D / 4), ch = 4 * (e % (D / 4));
                 float ms[kMaxCluster];
                 float m = -INFINITY, l = 0.f;
@@ -875,11 +910,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
         if (a.weigh) {
             // ---- the weights of this CTA's blocks
             if (tid < here) {
+                float ms[kMaxCluster], ls[kMaxCluster];
                 float m = -INFINITY, l = 0.f;
-                for (int y = 0; y < a.cluster; ++y) m = fmaxf(m, *cluster.map_shared_rank(&sm.mc[tid], y));
+#pragma unroll
+                for (int y = 0; y < kMaxCluster; ++y) {
+                    ms[y] = y < a.cluster ? *cluster.map_shared_rank(&sm.mc[tid], y) : -INFINITY;
+                    ls[y] = y < a.cluster ? *cluster.map_shared_rank(&sm.lc[tid], y) : 0.f;
+                    m = fmaxf(m, ms[y]);
+                }
                 const float safe = m == -INFINITY ? 0.f : m;
-                for (int y = 0; y < a.cluster; ++y)
-                    l = fmaf(ex2(*cluster.map_shared_rank(&sm.mc[tid], y) - safe), *cluster.map_shared_rank(&sm.lc[tid], y), l);
+#pragma unroll
+                for (int y = 0; y < kMaxCluster; ++y) l = fmaf(ex2(ms[y] - safe), ls[y], l);
                 sm.total[tid] = row_total(m, l);
             }
             __syncthreads();
