@@ -4,9 +4,9 @@
 //
 // Both come down to the n largest of up to 32768 numbers a head, ties to the
 // lowest index, listed in ascending order: one CTA a list holds the numbers'
-// order keys in shared memory and finds the n-th largest eight bits at a time,
+// order keys in shared memory and finds the n-th largest ten bits at a time,
 // from the highest bit in which any two keys differ (a histogram of the keys
-// that agree so far; starting at the top byte, which scores of one size share,
+// that agree so far; starting at the top bits, which scores of one size share,
 // every key would count in one bin).
 //
 // The score of block J for query q is a bound on its keys' products with q,
@@ -34,8 +34,11 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 
+constexpr int kBits = 10;  // of a pass: two bins a thread
+static_assert(1 << kBits == 2 * kThreads, "two bins a thread");
+
 struct SelectSmem {
-    uint32_t hist[256];
+    alignas(8) uint32_t hist[1 << kBits];
     uint32_t low[kWarps], high[kWarps], sum[kWarps], ties[kWarps];
     uint32_t bin, above, in_bin;
 };
@@ -90,23 +93,25 @@ __device__ void largest(const uint32_t *key, int count, int n, int32_t *list, Se
     int bits = 32 - __clz(low ^ high);  // bits not yet known of the n-th largest key
     uint32_t prefix = bits == 32 ? 0u : high >> bits << bits, want = (uint32_t)n;
     while (bits > 0) {
-        const int shift = max(0, bits - 8);
+        const int shift = max(0, bits - kBits);
         const uint32_t known = bits == 32 ? 0u : 0xffffffffu << bits;
-        if (tid < 256) sm.hist[tid] = 0;
+        *reinterpret_cast<uint2 *>(&sm.hist[2 * tid]) = make_uint2(0u, 0u);
         __syncthreads();
         for (int i = tid; i < count; i += kThreads) {
             const uint32_t x = key[i];
             if ((x & known) == prefix) atomicAdd(&sm.hist[(x & ~known) >> shift], 1u);
         }
         __syncthreads();
-        // thread t holds bin 255 - t, so that sums run from the highest bin down
-        const uint32_t mine = tid < 256 ? sm.hist[255 - tid] : 0u;
+        // thread t holds the t-th pair of bins from the top, so that sums run from the highest bin down
+        const int pair = kThreads - 1 - tid;
+        const uint2 mine = *reinterpret_cast<const uint2 *>(&sm.hist[2 * pair]);
         uint32_t total;
-        const uint32_t above = sum_before(mine, sm.sum, total);
-        if (above < want && above + mine >= want) {
-            sm.bin = (uint32_t)(255 - tid);
-            sm.above = above;
-            sm.in_bin = mine;
+        uint32_t above = sum_before(mine.x + mine.y, sm.sum, total);
+        if (above < want && above + mine.y + mine.x >= want) {
+            const bool upper = above + mine.y >= want;
+            sm.bin = (uint32_t)(2 * pair + upper);
+            sm.above = upper ? above : above + mine.y;
+            sm.in_bin = upper ? mine.y : mine.x;
         }
         __syncthreads();
         prefix |= sm.bin << shift;
@@ -158,8 +163,30 @@ __global__ void __launch_bounds__(kThreads)
     const int b = (int)(bh / c.H), h = (int)(bh % c.H);
     grid_dep_wait();
     grid_dep_launch();
-    int L = checked_length(lens, b, c.blocks, err);
-    if (L < 0) L = 0;
+    // ---- this lane's first blocks and query channels are on their way while the length is (within the cache, whatever
+    // the length)
+    const int part = tid % kLanes;
+    constexpr int kRow = kThreads / kLanes;  // blocks of a step
+    uint4 lo[kAtOnce], hi[kAtOnce];
+    float ks[kAtOnce];
+    auto load = [&](int j0, int end) {
+#pragma unroll
+        for (int y = 0; y < kAtOnce; ++y) {
+            const int j = j0 + y * kRow + tid / kLanes;
+            lo[y] = hi[y] = make_uint4(0, 0, 0, 0);
+            ks[y] = 0.f;
+            if (j < end) {
+                const long long at = bh * c.blocks + j;
+                const uint4 *e = reinterpret_cast<const uint4 *>(c.bounds + at * (2 * D));
+                lo[y] = e[part];
+                hi[y] = e[kLanes + part];
+                ks[y] = c.scales[2 * at];
+            }
+        }
+    };
+    const int step = kRow * kAtOnce;
+    load(rank * step, c.blocks);
+    const int L = max(0, checked_length(lens, b, c.blocks, err));
     const int last = L - Tq + r;  // the query's own position
     const int count = last < 0 ? 0 : min(L / kBlock, last / kBlock + 1);
     if (count > n) {  // (the same in all CTAs of the cluster)
@@ -191,24 +218,8 @@ __global__ void __launch_bounds__(kThreads)
         __syncthreads();
         // ---- the scores
         uint32_t *to = ctas > 1 ? cg::this_cluster().map_shared_rank(key, 0) : key;
-        const int part = tid % kLanes;
-        constexpr int kRow = kThreads / kLanes;  // blocks of a step
-        for (int j0 = rank * kRow * kAtOnce; j0 < count; j0 += ctas * kRow * kAtOnce) {
-            uint4 lo[kAtOnce], hi[kAtOnce];
-            float ks[kAtOnce];
-#pragma unroll
-            for (int y = 0; y < kAtOnce; ++y) {
-                const int j = j0 + y * kRow + tid / kLanes;
-                lo[y] = hi[y] = make_uint4(0, 0, 0, 0);
-                ks[y] = 0.f;
-                if (j < count) {
-                    const long long at = bh * c.blocks + j;
-                    const uint4 *e = reinterpret_cast<const uint4 *>(c.bounds + at * (2 * D));
-                    lo[y] = e[part];
-                    hi[y] = e[kLanes + part];
-                    ks[y] = c.scales[2 * at];
-                }
-            }
+        for (int j0 = rank * step; j0 < count; j0 += ctas * step) {
+            if (j0 != rank * step) load(j0, count);
             float best[kAtOnce];
             bool none[kAtOnce];
 #pragma unroll
