@@ -18,7 +18,12 @@ namespace {
 using namespace sm100;
 using namespace q8;
 
-constexpr int kThreads = 256;
+// Threads of a CTA: four or eight 16-byte chunks each of keys and values a
+// thread at D = 64 and 128, since most of a thread's work on two is what goes
+// with any number of them (128 threads against 256, append and read: 24.6 and
+// 27.8 us for 144 heads of 1024 tokens at D = 64, 96 and 102 us for 8 heads of
+// 16411, 12308 and 8206 tokens at D = 128).
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of bf16 pairs; NaN stays
@@ -219,8 +224,9 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---- read: positions starts[b] .. + n - 1 as they are held, in bf16 (zero
 // rows past the end).  One CTA takes one block of 64 positions.
+constexpr int kReadThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kReadThreads)
     read_kernel(const Q8Cache c, const int32_t *__restrict__ lens, const int32_t *__restrict__ starts, int n,
                 int touched, __nv_bfloat16 *__restrict__ k, __nv_bfloat16 *__restrict__ v, int *err) {
     constexpr int kChunks = D / 8;
@@ -248,7 +254,7 @@ __global__ void __launch_bounds__(kThreads)
         const long long at = bh * c.blocks + block;
         const uint8_t *kc = c.k_codes + at * (kBlock * D), *vc = c.v_codes + at * (kBlock * D);
         const float ks = c.scales[2 * at], vs = c.scales[2 * at + 1];
-        for (int e = tid; e < D * (kBlock / 16); e += kThreads) {
+        for (int e = tid; e < D * (kBlock / 16); e += kReadThreads) {
             const int ch = e / (kBlock / 16), q = 4 * (e % (kBlock / 16));
             const uint4 w = *reinterpret_cast<const uint4 *>(vc + ch * kBlock + 4 * q);
             sv[ch][q] = w.x;
@@ -256,7 +262,7 @@ __global__ void __launch_bounds__(kThreads)
             sv[ch][q + 2] = w.z;
             sv[ch][q + 3] = w.w;
         }
-        for (int e = tid; e < kBlock * kChunks; e += kThreads) {
+        for (int e = tid; e < kBlock * kChunks; e += kReadThreads) {
             const int t = e / kChunks, ch = 8 * (e % kChunks);
             if (p0 + t < first || p0 + t >= last) continue;
             const uint2 w = *reinterpret_cast<const uint2 *>(kc + key_offset<D>(t, ch));
@@ -268,7 +274,7 @@ __global__ void __launch_bounds__(kThreads)
             *reinterpret_cast<uint4 *>(ko + (p0 + t - start) * D + ch) = r;
         }
         __syncthreads();
-        for (int e = tid; e < (kBlock / 4) * kChunks; e += kThreads) {
+        for (int e = tid; e < (kBlock / 4) * kChunks; e += kReadThreads) {
             const int quad = e / kChunks, ch = 8 * (e % kChunks);
             uint32_t w[8];
 #pragma unroll
@@ -288,7 +294,7 @@ __global__ void __launch_bounds__(kThreads)
         return;
     }
     const __nv_bfloat16 *rk = c.recent_k + bh * kRing * D, *rv = c.recent_v + bh * kRing * D;
-    for (int e = tid; e < kBlock * kChunks; e += kThreads) {
+    for (int e = tid; e < kBlock * kChunks; e += kReadThreads) {
         const int t = e / kChunks, ch = 8 * (e % kChunks);
         const long long p = p0 + t;
         if (p < first || p >= last) continue;
@@ -312,13 +318,13 @@ cudaError_t q8_append(const Q8Cache &c, const __nv_bfloat16 *k, const TStrides &
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaError_t e = mark_main_start(li, st);
     if (e != cudaSuccess) return e;
-    const dim3 g((unsigned)grid), t(kThreads);
+    const dim3 g((unsigned)grid);
     if (c.D == 32)
-        e = launch_pdl(append_kernel<32>, g, t, 0, st, c, k, sk, v, sv, n, lens, new_lens, touched, err);
+        e = launch_pdl(append_kernel<32>, g, dim3(kThreads), 0, st, c, k, sk, v, sv, n, lens, new_lens, touched, err);
     else if (c.D == 64)
-        e = launch_pdl(append_kernel<64>, g, t, 0, st, c, k, sk, v, sv, n, lens, new_lens, touched, err);
+        e = launch_pdl(append_kernel<64>, g, dim3(kThreads), 0, st, c, k, sk, v, sv, n, lens, new_lens, touched, err);
     else
-        e = launch_pdl(append_kernel<128>, g, t, 0, st, c, k, sk, v, sv, n, lens, new_lens, touched, err);
+        e = launch_pdl(append_kernel<128>, g, dim3(kThreads), 0, st, c, k, sk, v, sv, n, lens, new_lens, touched, err);
     if (e != cudaSuccess) return e;
     li.kernels += 1;
     return mark_main_end(li, st);
@@ -331,7 +337,7 @@ cudaError_t q8_read(const Q8Cache &c, const int32_t *lens, const int32_t *starts
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaError_t e = mark_main_start(li, st);
     if (e != cudaSuccess) return e;
-    const dim3 g((unsigned)grid), t(kThreads);
+    const dim3 g((unsigned)grid), t(kReadThreads);
     if (c.D == 32)
         e = launch_pdl(read_kernel<32>, g, t, 0, st, c, lens, starts, n, touched, k, v, err);
     else if (c.D == 64)
