@@ -999,11 +999,16 @@ __global__ void __launch_bounds__(kJoinThreads) weight_kernel(const __grid_const
 }
 
 constexpr int kSms = 148;
-
-template <int D>
-int ctas_of(int nt) {
-    return kSms * (nt == 1 ? Cfg<D, 1>::kCtas : Cfg<D, 2>::kCtas);
-}
+// CTAs that the GPU holds at once in clusters of 1 .. 8, with up to 1, 2 and 3
+// CTAs an SM (cudaOccupancyMaxActiveClusters on B200: a cluster lies within a
+// part of the GPU, and the parts' sizes leave SMs over).
+constexpr int kRoom[3][kMaxCluster] = {{148, 148, 135, 132, 130, 132, 105, 120},
+                                       {296, 296, 279, 284, 280, 270, 259, 264},
+                                       {444, 444, 426, 416, 410, 426, 392, 384}};
+constexpr int ctas_of(int nt) { return nt == 1 ? Cfg<64, 1>::kCtas : Cfg<64, 2>::kCtas; }
+static_assert(Cfg<32, 1>::kCtas == Cfg<64, 1>::kCtas && Cfg<128, 1>::kCtas == Cfg<64, 1>::kCtas &&
+                  Cfg<32, 2>::kCtas == Cfg<64, 2>::kCtas && Cfg<128, 2>::kCtas == Cfg<64, 2>::kCtas,
+              "CTAs an SM holds do not depend on the head size");
 
 // Clusters (the CTAs of one, 0: none) or runs.  With clusters, each choice of
 // CTAs costs the rounds that the GPU needs for all of them times the blocks a
@@ -1016,15 +1021,16 @@ constexpr int kMostInClusters = 8;
 struct Shares {
     int cluster, runs;
 };
-Shares shares_for(long long tiles, int D, int nt, int blocks) {
-    const long long room = D == 32 ? ctas_of<32>(nt) : D == 64 ? ctas_of<64>(nt) : ctas_of<128>(nt);
+Shares shares_for(long long tiles, int nt, int blocks) {
+    const int(&held)[kMaxCluster] = kRoom[ctas_of(nt) - 1];
+    const long long room = held[0];
     if (tiles * (blocks + 1) > kMostInClusters * room * kWarps && tiles * (blocks + kPad + kOpen) < (1ll << 31))
         return Shares{0, (int)room};
     int best = 1;
     long long least = 0;
     for (int n = 1; n <= kMaxCluster; ++n) {
         if (n > 1 && (long long)(n - 1) * kWarps > blocks) break;  // warps without a block
-        const long long rounds = (tiles * n + room - 1) / room;
+        const long long rounds = (tiles * n + held[n - 1] - 1) / held[n - 1];
         const long long cost = rounds * ((blocks + (long long)n * kWarps - 1) / ((long long)n * kWarps) + kPerCta);
         if (n == 1 || cost < least) {
             least = cost;
@@ -1049,7 +1055,7 @@ Plan make_plan(const Q8Cache &c, int H, int Tq, int list_n, bool weight) {
     p.nt = p.rows > 8 ? 2 : 1;
     p.tiles = (p.rows + 8 * p.nt - 1) / (8 * p.nt);
     p.groups = (long long)c.B * c.H * (lists ? Tq : 1) * p.tiles;
-    p.shares = shares_for(p.groups, c.D, p.nt, lists && list_n < c.blocks ? list_n : c.blocks);
+    p.shares = shares_for(p.groups, p.nt, lists && list_n < c.blocks ? list_n : c.blocks);
     // a key head's rows in several tiles: the weights are summed by a kernel that finds their sums in the workspace
     if (weight && p.shares.cluster && p.tiles > 1)
         p.shares = Shares{0, kSms};
@@ -1069,7 +1075,8 @@ cudaError_t launch(const DecodeArgs &a, const Plan &p, cudaStream_t st, LaunchIn
     int dev = 0;
     cudaError_t e;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    // CTAs fill one SM after another, so a grid that leaves room asks for as much shared memory as keeps it spread out.
+    // CTAs fill one SM after another, so a grid that leaves room asks for as much shared memory as keeps it spread out
+    // (144 row tiles of 16 blocks in 288 CTAs: 8.9 us on 127 SMs, 7.9 us with two CTAs on each).
     const size_t smem_most = 227 * 1024;
     static std::atomic<unsigned long long> smem_set{0};
     if ((e = set_max_smem_once(reinterpret_cast<const void *>(decode_kernel<D, NT>), smem_most, dev, smem_set)) !=
@@ -1078,8 +1085,11 @@ cudaError_t launch(const DecodeArgs &a, const Plan &p, cudaStream_t st, LaunchIn
     const long long grid = a.cluster ? p.groups * a.cluster : a.runs;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     size_t smem = sizeof(Smem<D, NT>) + 128;
-    const long long on_sm = (grid + kSms - 1) / kSms;
-    if (on_sm < Cfg<D, NT>::kCtas) smem = smem_most / (size_t)on_sm / 1024 * 1024 - 1024;
+    for (int per = 1; per < Cfg<D, NT>::kCtas; ++per)
+        if (grid <= kRoom[per - 1][a.cluster ? a.cluster - 1 : 0]) {
+            smem = smem_most / per / 1024 * 1024 - 1024;
+            break;
+        }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);

@@ -325,6 +325,36 @@ def test_decode_from_one_to_many_heads(B, H, n):
     check_decode(q, o, lse, sequences(k, v, lens), lens, weight=c.weight.double().cpu().numpy(), label=f"B={B} H={H}")
 
 
+@pytest.mark.parametrize("D,B,H,G,tq,room", [(64, 40, 3, 1, 1, 400), (32, 70, 2, 2, 1, 400), (128, 5, 1, 12, 3, 4000),
+                                             (64, 3, 2, 1, 16, 4000), (64, 33, 1, 20, 1, 700), (64, 2, 2, 1, 2, 9000)])
+def test_decode_shared_out_by_the_lengths(D, B, H, G, tq, room):
+    """Caches with room for so much that CTAs take equal runs of all blocks: very unequal lengths, empty sequences at
+    the start, in the middle and at the end, more sequences than a warp has lanes, several row tiles, weights."""
+    lens = [(0, 1, 63, 64, 65, 700, 200, 1500, 0, 129)[(b + B) % 10] for b in range(B)]
+    k, v = tokens(B + D, B, H, 1500, D)
+    c, L = filled(k, v, lens, max_tokens=64 * room)
+    q = queries(B, B, H * G, tq, D)
+    seqs = sequences(k, v, lens)
+    for weight in (None, "set"):
+        o, lse = A.attn_q8_decode(q.to(dev()), c, L, weight=weight)
+        assert status() == 0
+        check_decode(q, o, lse, seqs, lens, weight=c.weight.double().cpu().numpy() if weight else None, label=f"runs {weight}")
+    o, lse = A.attn_q8_decode(q.to(dev()), c, 0 * L)
+    assert status() == 0 and (o == 0).all() and (lse == -INF).all()
+    bad = L.clone()
+    bad[B // 2] = 64 * room + 64
+    A.attn_q8_decode(q.to(dev()), c, bad)
+    assert status() == E_LENGTH
+    # lists long enough for the same, mostly -1
+    blocks = A.attn_q8_select(q.to(dev()), c, L, room)
+    o, lse = A.attn_q8_decode(q.to(dev()), c, L, blocks=blocks)
+    assert status() == 0
+    lists = blocks.cpu().numpy()
+    for b in range(B):
+        assert all((x >= 0).sum() <= lens[b] // 64 for x in lists[b].reshape(-1, room))
+    check_decode(q, o, lse, seqs, lens, label="lists of every block")
+
+
 @pytest.mark.parametrize("qs,ks,vs", [(100.0, 10.0, 1.0), (1e-3, 1e-3, 1e3), (1e10, 1e-10, 1e-20), (0.0, 1.0, 1.0),
                                       (1e-30, 1e30, 1e30), (20.0, 1.0, 0.0)])
 def test_decode_magnitudes(qs, ks, vs):
