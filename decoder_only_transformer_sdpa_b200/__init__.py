@@ -811,15 +811,15 @@ def attn_q8_evict(cache, lens, keep: int, sink: int = 0, recent: int = 1, out=No
         kp = kept.data_ptr()
     else:
         kp = _whole(kept, "kept", i32, shape, index)
-    if workspace is None:
-        need = cache.needs.get("evict")
-        if need is None:
-            need = cache.needs["evict"] = attn_q8_evict_workspace_bytes(cache)
-        made.append(workspace := cache.k_codes.new_empty(need))
-    elif not workspace.is_contiguous() or workspace.get_device() != index:
-        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+    wp, wn = None, 0
+    if workspace is None and op == lp:  # the only case that needs one
+        made.append(workspace := cache.k_codes.new_empty(attn_q8_evict_workspace_bytes(cache)))
+    if workspace is not None:
+        if not workspace.is_contiguous() or workspace.get_device() != index:
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _call(_lib.attn_q8_evict, "attn_q8_evict", index, stream, cache.ref, out.ref, lp, op, kp, int(keep), int(sink),
-          int(recent), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+          int(recent), wp, wn)
     if stream is not None:
         _used_on(stream, index, *made)
     return lens_out, kept

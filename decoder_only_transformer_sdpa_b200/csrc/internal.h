@@ -168,9 +168,10 @@ size_t q8_decode_workspace(const Q8Cache &c, int H, int Tq, int list_n, bool wei
 cudaError_t q8_decode(const Q8Cache &c, const Q8Decode &d, int *err, cudaStream_t st, LaunchInfo &li);
 cudaError_t q8_select(const Q8Cache &c, const __nv_bfloat16 *q, const TStrides &sq, const int32_t *lens,
                       int32_t *list, int list_n, int H, int Tq, int *err, cudaStream_t st, LaunchInfo &li);
-// workspace: 2 * B * Hkv ints.
+// Workspace of q8_evict, which uses it only where lens_out == lens.
+size_t q8_evict_workspace(const Q8Cache &c);
 cudaError_t q8_evict(const Q8Cache &src, const Q8Cache &dst, const int32_t *lens, int32_t *lens_out, int32_t *kept,
-                     int keep, int sink, int recent, int *workspace, int *err, cudaStream_t st, LaunchInfo &li);
+                     int keep, int sink, int recent, void *workspace, int *err, cudaStream_t st, LaunchInfo &li);
 
 // ---- what every entry point does: the armed events of the call being made,
 // the device check with the error word's address, the end of a call.

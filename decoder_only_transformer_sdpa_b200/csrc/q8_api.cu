@@ -175,7 +175,10 @@ ATTN_API int attn_q8_select(const attn_q8_cache *cache, const void *q, const int
 
 ATTN_API size_t attn_q8_evict_workspace_bytes(const attn_q8_cache *cache) {
     if (!cache || check_sizes(*cache) != ATTN_OK) return 0;
-    return ((size_t)cache->B * cache->H * 2 * sizeof(int) + 255) / 256 * 256;
+    Q8Cache c{};
+    c.B = cache->B;
+    c.H = cache->H;
+    return (q8_evict_workspace(c) + 255) / 256 * 256;
 }
 
 ATTN_API int attn_q8_evict(const attn_q8_cache *cache, const attn_q8_cache *out, const int32_t *lens,
@@ -200,11 +203,11 @@ ATTN_API int attn_q8_evict(const attn_q8_cache *cache, const attn_q8_cache *out,
     if (same[0] && (c.blocks != d.blocks || c.bounds != d.bounds)) return ATTN_ERR_OPTION;
     if (!same[0] && c.bounds && c.bounds == d.bounds) return ATTN_ERR_OPTION;
     if (!aligned(lens, 4) || !aligned(lens_out, 4) || !aligned(kept, 4)) return ATTN_ERR_ALIGN;
-    if (!workspace || workspace_bytes < attn_q8_evict_workspace_bytes(cache) || !aligned(workspace, 256))
+    if (lens_out == lens &&
+        (!workspace || workspace_bytes < attn_q8_evict_workspace_bytes(cache) || !aligned(workspace, 256)))
         return ATTN_ERR_WORKSPACE;
     int *err = nullptr;
     if ((st = device_setup(&err)) != ATTN_OK) return st;
-    return finish(q8_evict(c, d, lens, lens_out, kept, keep, sink, recent, static_cast<int *>(workspace), err, stream,
-                           li),
+    return finish(q8_evict(c, d, lens, lens_out, kept, keep, sink, recent, workspace, err, stream, li),
                   li);
 }

@@ -29,7 +29,7 @@
 //   * little work: the CTAs of a cluster share a row tile, each block going to
 //     the next of their warps, and they join their results through distributed
 //     shared memory: one launch;
-//   * much of it: as many CTAs as the GPU holds take equal runs of all blocks of
+//   * much of it: CTAs that fill the GPU twice take equal runs of all blocks of
 //     all row tiles, whatever the sequences' lengths (which only the kernel
 //     knows); a second kernel joins what the runs left of each row tile.
 //
@@ -1017,7 +1017,10 @@ static_assert(Cfg<32, 1>::kCtas == Cfg<64, 1>::kCtas && Cfg<128, 1>::kCtas == Cf
 // holds, runs are at least as fast and even out unequal lengths: at 1.4 blocks a
 // warp clusters take 7.9 us and runs 11.3 (144 row tiles of 16 blocks), at 7.4
 // both 22.5 (200 of 64), at 55 clusters 98 and runs 87 (192 of up to 512).
-constexpr int kMostInClusters = 8;
+// Two runs for each CTA that the GPU holds let an SM that is quicker than others
+// take more of them (85.2 us with one, 83.9 with two, 84.3 with four at 55 blocks
+// a warp).
+constexpr int kMostInClusters = 8, kRunsOfCta = 2;
 struct Shares {
     int cluster, runs;
 };
@@ -1025,7 +1028,7 @@ Shares shares_for(long long tiles, int nt, int blocks) {
     const int(&held)[kMaxCluster] = kRoom[ctas_of(nt) - 1];
     const long long room = held[0];
     if (tiles * (blocks + 1) > kMostInClusters * room * kWarps && tiles * (blocks + kPad + kOpen) < (1ll << 31))
-        return Shares{0, (int)room};
+        return Shares{0, (int)(kRunsOfCta * room)};
     int best = 1;
     long long least = 0;
     for (int n = 1; n <= kMaxCluster; ++n) {

@@ -257,13 +257,21 @@ __global__ void __launch_bounds__(kThreads)
     if (rank == 0) largest(key, count, n, lists + (long long)which * n, sm);
 }
 
-// ---- by weight.  One CTA a key head; `state` takes twice the count of kept
-// blocks, plus one if an odd count goes, and the sequence's new length (-1
-// where the length is out of range): the lengths themselves may be overwritten
-// while the blocks move.
+// What becomes of a sequence of length L (-1: out of range, it stays as it is).
+struct Fate {
+    int kept, length, odd;  // blocks it keeps, its new length, whether an odd count of blocks goes
+};
+__device__ __forceinline__ Fate fate_of(int L, int keep) {
+    if (L < 0) return Fate{0, -1, 0};
+    const int closed = L / kBlock, kept = min(closed, keep);
+    return Fate{kept, kept * kBlock + L % kBlock, (closed - kept) & 1};
+}
+
+// ---- by weight.  One CTA a key head.  Where the new lengths take the old ones'
+// place, `fates` keeps what the kernel that moves the blocks has to know of them.
 __global__ void __launch_bounds__(kThreads)
     keep_kernel(const Q8Cache c, const int32_t *__restrict__ lens, int32_t *__restrict__ kept, int keep, int sink,
-                int recent, int *__restrict__ state, int *err) {
+                int recent, Fate *__restrict__ fates, int *err) {
     __shared__ SelectSmem sm;
     extern __shared__ uint32_t key[];
     const long long bh = blockIdx.x;
@@ -279,11 +287,7 @@ __global__ void __launch_bounds__(kThreads)
         __syncthreads();
     }
     largest(key, closed, keep, kept + bh * keep, sm);
-    if (threadIdx.x == 0) {
-        const int left = closed < keep ? closed : keep;
-        state[2 * bh] = L < 0 ? 0 : 2 * left + ((closed - left) & 1);
-        state[2 * bh + 1] = L < 0 ? -1 : left * kBlock + L % kBlock;
-    }
+    if (fates && threadIdx.x == 0) fates[bh] = fate_of(L, keep);
 }
 
 // ---- the kept blocks to the front (of the same cache, or of another one).
@@ -299,7 +303,7 @@ constexpr int kRounds = 8;
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads)
     move_kernel(const Q8Cache c, const Q8Cache d, const int32_t *__restrict__ lens, int32_t *__restrict__ lens_out,
-                const int32_t *__restrict__ kept, int keep, const int *__restrict__ state, int chunks, int *err) {
+                const int32_t *__restrict__ kept, int keep, const Fate *__restrict__ fates, int chunks, int *err) {
     constexpr int kBytes = kBlock * D;            // codes of a block's keys
     constexpr int kSlices = 2 * kBytes / kSlice;
     const int tid = threadIdx.x;
@@ -311,8 +315,9 @@ __global__ void __launch_bounds__(kMoveThreads)
     const bool same = c.k_codes == d.k_codes;
     grid_dep_wait();
     grid_dep_launch();
-    const int count = state[2 * bh] >> 1, length = state[2 * bh + 1];
-    const bool odd = state[2 * bh] & 1;
+    const int L = fates ? 0 : lens[b];
+    const Fate fate = fates ? fates[bh] : fate_of(L >= 0 && L / kBlock <= c.blocks ? L : -1, keep);
+    const int count = fate.kept;
     const int32_t *from = kept + bh * keep;
     // this chunk's blocks: all of them when they move within one cache
     const int per = (keep + chunks - 1) / chunks;
@@ -369,12 +374,12 @@ __global__ void __launch_bounds__(kMoveThreads)
         }
     }
     if (chunk != 0) return;
-    if (h == 0 && tid == 0) lens_out[b] = length < 0 ? lens[b] : length;
-    if (length < 0) return;
+    if (h == 0 && tid == 0) lens_out[b] = fate.length < 0 ? lens[b] : fate.length;
+    if (fate.length < 0) return;
     // ---- the ring: position p lies in row p % 128, so its halves change places when an odd count of blocks goes
-    if (same && !odd) return;
+    if (same && !fate.odd) return;
     constexpr int kChunks = kBlock * D / 8;  // 16-byte chunks of a half
-    const int other = odd ? kChunks : 0;
+    const int other = fate.odd ? kChunks : 0;
     const uint4 *sk = reinterpret_cast<const uint4 *>(c.recent_k) + bh * 2 * kChunks;
     const uint4 *sv = reinterpret_cast<const uint4 *>(c.recent_v) + bh * 2 * kChunks;
     uint4 *dk = reinterpret_cast<uint4 *>(d.recent_k) + bh * 2 * kChunks;
@@ -389,6 +394,8 @@ __global__ void __launch_bounds__(kMoveThreads)
 }
 
 }  // namespace
+
+size_t q8_evict_workspace(const Q8Cache &c) { return (size_t)c.B * c.H * sizeof(Fate); }
 
 cudaError_t q8_select(const Q8Cache &c, const __nv_bfloat16 *q, const TStrides &sq, const int32_t *lens,
                       int32_t *list, int list_n, int H, int Tq, int *err, cudaStream_t st, LaunchInfo &li) {
@@ -437,7 +444,8 @@ cudaError_t q8_select(const Q8Cache &c, const __nv_bfloat16 *q, const TStrides &
 }
 
 cudaError_t q8_evict(const Q8Cache &src, const Q8Cache &dst, const int32_t *lens, int32_t *lens_out, int32_t *kept,
-                     int keep, int sink, int recent, int *workspace, int *err, cudaStream_t st, LaunchInfo &li) {
+                     int keep, int sink, int recent, void *workspace, int *err, cudaStream_t st, LaunchInfo &li) {
+    Fate *fates = lens_out == lens ? static_cast<Fate *>(workspace) : nullptr;
     int dev = 0;
     cudaError_t e;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
@@ -453,16 +461,16 @@ cudaError_t q8_evict(const Q8Cache &src, const Q8Cache &dst, const int32_t *lens
     const long long grid = heads * slices * chunks;
     if (heads > 0x7fffffffLL || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     if ((e = launch_pdl(keep_kernel, dim3((unsigned)heads), dim3(kThreads), (size_t)src.blocks * 4, st, src, lens, kept,
-                        keep, sink, recent, workspace, err)) != cudaSuccess)
+                        keep, sink, recent, fates, err)) != cudaSuccess)
         return e;
     if ((e = mark_main_start(li, st)) != cudaSuccess) return e;
     const dim3 g((unsigned)grid), t(kMoveThreads);
     if (src.D == 32)
-        e = launch_pdl(move_kernel<32>, g, t, 0, st, src, dst, lens, lens_out, kept, keep, workspace, chunks, err);
+        e = launch_pdl(move_kernel<32>, g, t, 0, st, src, dst, lens, lens_out, kept, keep, fates, chunks, err);
     else if (src.D == 64)
-        e = launch_pdl(move_kernel<64>, g, t, 0, st, src, dst, lens, lens_out, kept, keep, workspace, chunks, err);
+        e = launch_pdl(move_kernel<64>, g, t, 0, st, src, dst, lens, lens_out, kept, keep, fates, chunks, err);
     else
-        e = launch_pdl(move_kernel<128>, g, t, 0, st, src, dst, lens, lens_out, kept, keep, workspace, chunks, err);
+        e = launch_pdl(move_kernel<128>, g, t, 0, st, src, dst, lens, lens_out, kept, keep, fates, chunks, err);
     if (e != cudaSuccess) return e;
     li.kernels += 2;
     return mark_main_end(li, st);

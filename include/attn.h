@@ -401,7 +401,8 @@ int attn_q8_decode(const attn_q8_cache *cache, const void *q, void *o, float *ls
 int attn_q8_select(const attn_q8_cache *cache, const void *q, const int32_t *lens, int32_t *blocks,
                    int n, int H, int Tq, const attn_strides *strides, cudaStream_t stream);
 
-/* Bytes of device workspace attn_q8_evict needs; 0 on a bad shape. */
+/* Bytes of device workspace attn_q8_evict needs where lens_out is lens; 0 on a
+ * bad shape. */
 size_t attn_q8_evict_workspace_bytes(const attn_q8_cache *cache);
 
 /* Drops closed blocks until each sequence and head has at most `keep` (>= 1) of
@@ -414,7 +415,7 @@ size_t attn_q8_evict_workspace_bytes(const attn_q8_cache *cache);
  * * 64 + lens[b] % 64; kept int32 [B, H, keep] the places the blocks came from,
  * ascending, -1 behind the last.  Heads keep different blocks, all of them
  * equally many.  workspace: as attn_q8_evict_workspace_bytes, 256-byte
- * aligned.  Two launches. */
+ * aligned, where lens_out is lens; else it is not looked at.  Two launches. */
 int attn_q8_evict(const attn_q8_cache *cache, const attn_q8_cache *out, const int32_t *lens,
                   int32_t *lens_out, int32_t *kept, int keep, int sink, int recent, void *workspace,
                   size_t workspace_bytes, cudaStream_t stream);

@@ -142,6 +142,7 @@ OTHER = dict(k_codes=11 * P, v_codes=12 * P, scales=13 * P, bounds=14 * P, weigh
     (dict(out=cache(**{**OTHER, "recent_v": 7 * P})), E_OPTION), (dict(out=cache(**{**OTHER, "bounds": 4 * P})), E_OPTION),
     (dict(out=cache(**{**OTHER, "weight": 5 * P})), E_OPTION), (dict(out=cache(blocks=3)), E_OPTION),
     (dict(out=cache(bounds=None)), E_OPTION), (dict(lens_out=P + 2), E_ALIGN), (dict(kept=P + 2), E_ALIGN),
+    # (lens_out is lens: only then is there a workspace)
     (dict(ws=None), E_WS), (dict(ws=P + 128), E_WS), (dict(ws_bytes=40), E_WS),
 ])
 def test_evict_refusals(kw, expect):
@@ -163,7 +164,7 @@ def test_workspace_sizes():
     some = ws(one, 1, 1)  # one head over millions of tokens: several clusters
     assert some > 0 and some % 256 == 0
     assert ws(one, 1, 1, None, 8, 0) == 0 and ws(one, 1, 1, None, 0, 2) > 4 * 32768
-    assert A.lib().attn_q8_evict_workspace_bytes(ctypes.byref(c)) == up(7 * 30 * 8)
+    assert A.lib().attn_q8_evict_workspace_bytes(ctypes.byref(c)) == up(7 * 30 * 12)
     assert A.lib().attn_q8_evict_workspace_bytes(ctypes.byref(cache(H=0))) == 0
 
 
