@@ -551,7 +551,7 @@ class Q8Cache:
     Sequence lengths are the caller's: an int32 CUDA tensor ``lens`` [B] that
     counts the new tokens before they are appended."""
     __slots__ = ("k_codes", "v_codes", "scales", "bounds", "weight", "recent_k", "recent_v", "B", "H",
-                 "blocks", "D", "device", "index", "struct", "ref", "needs", "batch", "types")
+                 "blocks", "D", "device", "index", "struct", "ref", "needs", "batch", "types", "blanks")
 
     def __init__(self, k_codes, v_codes, scales, bounds, weight, recent_k, recent_v):
         torch = _torch()
@@ -579,6 +579,18 @@ class Q8Cache:
         self.index = self.device.index
         self.needs = {}  # workspace bytes by (query heads, new tokens, list length, weights)
         self.batch, self.types = (B,), (torch.bfloat16, torch.int32, torch.float32)
+        self.blanks = {}  # one-element tensors that stand for the outputs' types and shapes
+
+    def new(self, dtype, shape):
+        """A new contiguous tensor on the cache's device.  (empty_like of an
+        expanded one-element tensor costs the host half of new_empty.)"""
+        torch = _torch()
+        blank = self.blanks.get((dtype, shape))
+        if blank is None:
+            if len(self.blanks) > 100:
+                self.blanks.clear()
+            blank = self.blanks[dtype, shape] = torch.empty(1, dtype=dtype, device=self.device).expand(shape)
+        return torch.empty_like(blank, memory_format=torch.contiguous_format)
 
     @classmethod
     def empty(cls, B: int, H: int, D: int, max_tokens: int, device="cuda", bounds: bool = True,
@@ -656,7 +668,7 @@ def attn_q8_append(cache, k, v, lens, new_lens=None, stream=None) -> None:
     ones; None: all n)."""
     index = _check_cache(cache)
     bf16, i32, _ = cache.types
-    n = _shape4(k)[2]
+    n = k.shape[2] if k.dim() == 4 else _shape4(k)
     shape = (cache.B, cache.H, n, cache.D)
     kp, vp = _view(k, "k", bf16, shape, index), _view(v, "v", bf16, shape, index)
     lp = _whole(lens, "lens", i32, cache.batch, index)
@@ -677,12 +689,12 @@ def attn_q8_read(cache, lens, n: int, starts=None, k=None, v=None, stream=None):
     sp = None if starts is None else _whole(starts, "starts", i32, cache.batch, index)
     made = []
     if k is None:
-        made.append(k := cache.recent_k.new_empty(shape))
+        made.append(k := cache.new(bf16, shape))
         kp = k.data_ptr()
     else:
         kp = _whole(k, "k", bf16, shape, index)
     if v is None:
-        made.append(v := cache.recent_k.new_empty(shape))
+        made.append(v := cache.new(bf16, shape))
         vp = v.data_ptr()
     else:
         vp = _whole(v, "v", bf16, shape, index)
@@ -710,7 +722,7 @@ def attn_q8_decode(q, cache, lens, o=None, lse=None, scale: Optional[float] = No
     Returns (O [B, Hq, Tq, D], lse [B, Hq, Tq])."""
     index = _check_cache(cache)
     bf16, i32, f32 = cache.types
-    _, H, Tq, D = _shape4(q)
+    _, H, Tq, D = q.shape if q.dim() == 4 else _shape4(q)
     keep = _Q8_WEIGHT.get(weight)
     if keep is None:
         raise ValueError("weight must be None, 'set' or 'add'")
@@ -720,12 +732,12 @@ def attn_q8_decode(q, cache, lens, o=None, lse=None, scale: Optional[float] = No
     plain = q.is_contiguous()
     made = []
     if o is None:
-        made.append(o := _torch().empty_like(q) if plain else q.new_empty(shape))
+        made.append(o := cache.new(bf16, shape))
         op = o.data_ptr()
     else:
         op = _view(o, "o", bf16, shape, index)
     if lse is None:
-        made.append(lse := q.new_empty(shape[:3], dtype=f32))
+        made.append(lse := cache.new(f32, shape[:3]))
         ep = lse.data_ptr()
     else:
         ep = _whole(lse, "lse", f32, shape[:3], index)
@@ -761,7 +773,7 @@ def attn_q8_select(q, cache, lens, n: int, blocks=None, stream=None):
     int32 [B, H, Tq, n], ascending, -1 behind the last."""
     index = _check_cache(cache)
     bf16, i32, _ = cache.types
-    _, H, Tq, _ = _shape4(q)
+    _, H, Tq, _ = q.shape if q.dim() == 4 else _shape4(q)
     if n < 1:
         raise AttnError(-2, "attn_q8_select")
     shape = (cache.B, cache.H, Tq, int(n))
@@ -769,7 +781,7 @@ def attn_q8_select(q, cache, lens, n: int, blocks=None, stream=None):
     lp = _whole(lens, "lens", i32, cache.batch, index)
     made = []
     if blocks is None:
-        made.append(blocks := lens.new_empty(shape))
+        made.append(blocks := cache.new(i32, shape))
         bp = blocks.data_ptr()
     else:
         bp = _whole(blocks, "blocks", i32, shape, index)
@@ -801,13 +813,13 @@ def attn_q8_evict(cache, lens, keep: int, sink: int = 0, recent: int = 1, out=No
     lp = _whole(lens, "lens", i32, cache.batch, index)
     made = []
     if lens_out is None:
-        made.append(lens_out := lens.new_empty(cache.batch))
+        made.append(lens_out := cache.new(i32, cache.batch))
         op = lens_out.data_ptr()
     else:
         op = _whole(lens_out, "lens_out", i32, cache.batch, index)
     shape = (cache.B, cache.H, int(keep))
     if kept is None:
-        made.append(kept := lens.new_empty(shape))
+        made.append(kept := cache.new(i32, shape))
         kp = kept.data_ptr()
     else:
         kp = _whole(kept, "kept", i32, shape, index)
