@@ -3,6 +3,7 @@
 // kernels.  Nothing here computes attention; every step runs in a kernel.
 #include "../../include/attn.h"
 #include "internal.h"
+#include "q8.h"
 
 #include <math.h>
 #include <mutex>

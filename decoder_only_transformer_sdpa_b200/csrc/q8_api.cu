@@ -1,7 +1,7 @@
 // q8_api.cu -- the extern "C" entry points of the 8-bit block cache
 // (declared in include/attn.h): argument checks and dispatch to the kernels.
 #include "../../include/attn.h"
-#include "internal.h"
+#include "q8.h"
 
 #include <math.h>
 

@@ -23,7 +23,7 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
-#include "internal.h"
+#include "q8.h"
 #include "sm100.cuh"
 
 namespace attn {
