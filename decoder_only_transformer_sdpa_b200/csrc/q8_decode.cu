@@ -51,9 +51,6 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kPShift = 7.f;   // P is held as 2^7 exp2(s - m)
 constexpr float kSlack = 8.f;    // how far a score may pass m before m moves
 constexpr int kMaxCluster = 8;   // portable cluster size
-// What a CTA costs beside its blocks, and the joining kernel, in the time a
-// warp takes for a block.
-constexpr int kPerCta = 3;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm(
@@ -96,9 +93,9 @@ struct Cfg {
     static constexpr int kCtas = NT == 1 ? 3 : 2;
     static constexpr int kHalves = D == 128 ? 2 : 1;  // slots of a block
     static constexpr int kSlots = D == 32 ? 4 : (NT == 1 ? 2 : 3);
-    static constexpr bool kQueriesInSmem = NT == 2;  // else in registers
+    static constexpr bool kQueriesInSmem = NT > 1;  // else in registers
     // tiles of 16 tokens (keys) or 16 channels (values) whose sums a warp forms side by side
-    static constexpr int kAtOnce = D == 32 ? 2 : 4 / NT;
+    static constexpr int kAtOnce = NT == 4 ? 1 : D == 32 ? 2 : 4 / NT;
 };
 
 // Layout of the workspace: what each run left of a row tile (its unnormalised
@@ -176,11 +173,11 @@ __device__ __forceinline__ Where where(const DecodeArgs &a, unsigned index) {
     return w;
 }
 // ---- runs.  All row tiles' work is laid end to end in units of a block's time:
-// kPad units that stand for what a CTA spends on a row tile beside its blocks,
-// the places of the list or the closed blocks, and kOpen units for an open block.
-// Run r takes the units from r * units_of_run on.  A row tile without a block is
-// nobody's.
-constexpr int kPad = 4, kOpen = 2;
+// kPad units that stand for what a CTA's warps spend on a row tile beside its
+// blocks, the places of the list or the closed blocks, and kOpen units for an
+// open block.  Run r takes the units from r * units_of_run on, at least kLeastRun
+// of them.  A row tile without a token is nobody's.
+constexpr int kPad = 12, kOpen = 2, kLeastRun = 8;
 __device__ __forceinline__ unsigned units_of(const DecodeArgs &a, int b) {
     int L = a.lens[b];
     if (L < 0 || L / kBlock > a.c.blocks) L = 0;
@@ -206,7 +203,7 @@ __device__ __forceinline__ unsigned units_of_run(const DecodeArgs &a, unsigned m
     unsigned all = mine;
     for (int i = 32 + (threadIdx.x & 31); i < a.c.B; i += 32) all += units_of(a, i);
     all = __reduce_add_sync(0xffffffffu, all) * tiles_of_sequence(a);
-    return max(1u, (all + a.runs - 1) / (unsigned)a.runs);
+    return max((unsigned)kLeastRun, (all + a.runs - 1) / (unsigned)a.runs);
 }
 // The row tile with unit u, and u's place in it and the tile's units; false: u
 // lies behind all of them.  The whole warp calls it.
@@ -937,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
 
 // Joins what the runs left of a row: blockIdx.x is its row tile, blockIdx.y its
 // place there.  A row of D / 4 threads takes every kParts-th run.
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
 template <int D, int NT>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ DecodeArgs a) {
     constexpr int kRows = 8 * NT, kLanes = D / 4, kParts = kJoinThreads / kLanes;
@@ -984,7 +981,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 }
 
 // The blocks' weights where a key head's rows are joined from runs.
-// blockIdx.x: key head; blockIdx.y: 128 blocks at a time.
+// blockIdx.x: key head; blockIdx.y: 256 blocks at a time.
 template <int NT>
 __global__ void __launch_bounds__(kJoinThreads) weight_kernel(const __grid_constant__ DecodeArgs a) {
     constexpr int kRows = 8 * NT;
@@ -1005,30 +1002,29 @@ constexpr int kSms = 148;
 constexpr int kRoom[3][kMaxCluster] = {{148, 148, 135, 132, 130, 132, 105, 120},
                                        {296, 296, 279, 284, 280, 270, 259, 264},
                                        {444, 444, 426, 416, 410, 426, 392, 384}};
-constexpr int ctas_of(int nt) { return nt == 1 ? Cfg<64, 1>::kCtas : Cfg<64, 2>::kCtas; }
+constexpr int ctas_of(int nt) { return nt == 1 ? Cfg<64, 1>::kCtas : Cfg<64, 2>::kCtas; }  // (2 and 4 alike)
 static_assert(Cfg<32, 1>::kCtas == Cfg<64, 1>::kCtas && Cfg<128, 1>::kCtas == Cfg<64, 1>::kCtas &&
                   Cfg<32, 2>::kCtas == Cfg<64, 2>::kCtas && Cfg<128, 2>::kCtas == Cfg<64, 2>::kCtas,
               "CTAs an SM holds do not depend on the head size");
 
-// Clusters (the CTAs of one, 0: none) or runs.  With clusters, each choice of
-// CTAs costs the rounds that the GPU needs for all of them times the blocks a
-// warp then reads, plus what a CTA costs beside its blocks.  Where all row tiles
-// together have more than kMostInClusters blocks for each warp that the GPU
-// holds, runs are at least as fast and even out unequal lengths: at 1.4 blocks a
-// warp clusters take 7.9 us and runs 11.3 (144 row tiles of 16 blocks), at 7.4
-// both 22.5 (200 of 64), at 55 clusters 98 and runs 87 (192 of up to 512).
-// Two runs for each CTA that the GPU holds let an SM that is quicker than others
-// take more of them (85.2 us with one, 83.9 with two, 84.3 with four at 55 blocks
-// a warp).
-constexpr int kMostInClusters = 8, kRunsOfCta = 2;
+// Clusters (the CTAs of one, 0: none) or runs, by what each costs in the time a
+// warp takes for a block, as if every sequence filled its cache.  Clusters of n
+// CTAs a row tile: the rounds that the GPU needs for all of them times the blocks
+// a warp reads and kPerCta beside them.  Runs: each warp's even share of all units
+// and kPerRuns for finding them and joining what they leave.  Measured (us,
+// clusters / runs; row tiles x blocks): 144 x 16 7.9 / 9.6, 200 x 64 22 / 23,
+// 32 x 257 (head size 128, 16 rows) 33 / 37, 432 x 24 (16 rows) 34 / 46, 6 x 265
+// (16 rows) 17 / 14.5, 1 x 2048 66 / 22, 192 x up to 512 98 / 84.
+constexpr int kPerCta = 3, kPerRuns = 5;
+// Where a run is long, two for each CTA that the GPU holds let an SM that is
+// quicker than others take more of them (83.9 us against 85.2 at 230 units a run;
+// 38.9 against 37.4 at 56).
+constexpr int kLongRun = 100;
 struct Shares {
     int cluster, runs;
 };
 Shares shares_for(long long tiles, int nt, int blocks) {
     const int(&held)[kMaxCluster] = kRoom[ctas_of(nt) - 1];
-    const long long room = held[0];
-    if (tiles * (blocks + 1) > kMostInClusters * room * kWarps && tiles * (blocks + kPad + kOpen) < (1ll << 31))
-        return Shares{0, (int)(kRunsOfCta * room)};
     int best = 1;
     long long least = 0;
     for (int n = 1; n <= kMaxCluster; ++n) {
@@ -1040,6 +1036,8 @@ Shares shares_for(long long tiles, int nt, int blocks) {
             best = n;
         }
     }
+    const long long units = tiles * (blocks + kPad + kOpen), each = units / held[0];
+    if (units < (1ll << 31) && each / kWarps + 1 + kPerRuns < least) return Shares{0, held[0] * (each >= kLongRun ? 2 : 1)};
     return Shares{best, 0};
 }
 
@@ -1055,7 +1053,7 @@ Plan make_plan(const Q8Cache &c, int H, int Tq, int list_n, bool weight) {
     Plan p;
     const int G = H / c.H;
     p.rows = lists ? G : G * Tq;
-    p.nt = p.rows > 8 ? 2 : 1;
+    p.nt = p.rows > 16 && c.D < 128 ? 4 : p.rows > 8 ? 2 : 1;
     p.tiles = (p.rows + 8 * p.nt - 1) / (8 * p.nt);
     p.groups = (long long)c.B * c.H * (lists ? Tq : 1) * p.tiles;
     p.shares = shares_for(p.groups, p.nt, lists && list_n < c.blocks ? list_n : c.blocks);
@@ -1164,8 +1162,10 @@ cudaError_t q8_decode(const Q8Cache &c, const Q8Decode &d, int *err, cudaStream_
     if (c.D == DD && p.nt == NN) return launch<DD, NN>(a, p, st, li);
     ATTN_Q8_CASE(32, 1)
     ATTN_Q8_CASE(32, 2)
+    ATTN_Q8_CASE(32, 4)
     ATTN_Q8_CASE(64, 1)
     ATTN_Q8_CASE(64, 2)
+    ATTN_Q8_CASE(64, 4)
     ATTN_Q8_CASE(128, 1)
     ATTN_Q8_CASE(128, 2)
 #undef ATTN_Q8_CASE
