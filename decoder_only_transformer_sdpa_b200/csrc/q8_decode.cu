@@ -79,6 +79,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
+__device__ __forceinline__ float lg2(float x) {  // off by 2^-22 at most
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -106,7 +111,7 @@ struct Parts {
     float *o;    // [run + tile][rows][D]
     float2 *ml;  // [run + tile][rows]
     float *total;  // [tile][rows] log2 of each row's sum (with weights)
-    float *lb;   // [B * Hkv][R][blocks]
+    float *lb;   // [B * Hkv][blocks][R]
 };
 
 template <int D, int NT>
@@ -460,12 +465,23 @@ __device__ __forceinline__ void write_row(const DecodeArgs &a, const Where &w, i
 // log2 of a row's sum, in the units of the blocks' sums; a row that sees nothing gives nothing.
 __device__ __forceinline__ float row_total(float m, float l) { return l == 0.f ? INFINITY : m + log2f(l); }
 
-// weight[j] (+)= sum over the rows of exp(block j's log-sum - the row's log-sum).
+// weight[j] (+)= sum over the rows of exp(block j's log-sum - the row's log-sum),
+// by eight consecutive lanes a block (all lanes of a warp call it; j < 0: none).
+constexpr int kWeightLanes = 8;
 __device__ __forceinline__ void write_weight(const DecodeArgs &a, long long bh, int j, const float *total) {
+    const int part = threadIdx.x % kWeightLanes;
     float sum = 0.f;
-    for (int row = 0; row < a.rows; ++row) sum += ex2(a.part.lb[(bh * a.rows + row) * a.c.blocks + j] - total[row]);
-    float *out = a.c.weight + bh * a.c.blocks + j;
-    *out = a.weight == 2 ? *out + sum : sum;
+    if (j >= 0) {
+        const float *lb = a.part.lb + (bh * a.c.blocks + j) * a.rows;
+#pragma unroll 4
+        for (int row = part; row < a.rows; row += kWeightLanes) sum += ex2(lb[row] - total[row]);
+    }
+#pragma unroll
+    for (int off = 1; off < kWeightLanes; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (j >= 0 && part == 0) {
+        float *out = a.c.weight + bh * a.c.blocks + j;
+        *out = a.weight == 2 ? *out + sum : sum;
+    }
 }
 
 template <int D, int NT>
@@ -761,8 +777,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
                         for (int off = 4; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
                         const int row = w.tile * kRows + nt * 8 + 2 * t + x;
                         if (g == 0 && row < a.rows)
-                            a.part.lb[(w.bh * a.rows + row) * a.c.blocks + id] =
-                                v == 0.f ? -INFINITY : st.m[nt][x] + log2f(v);
+                            a.part.lb[(w.bh * a.c.blocks + id) * a.rows + row] =
+                                v == 0.f ? -INFINITY : st.m[nt][x] + lg2(v);
                     }
             }
             uint32_t p[4][NT][2];
@@ -922,9 +938,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
             }
             __syncthreads();
             // places rank * kWarps + (0 .. kWarps - 1) + a multiple of step are this CTA's
-            for (int e = tid; (e / kWarps) * step + rank * kWarps < closed; e += kThreads) {
-                const int j = (e / kWarps) * step + rank * kWarps + e % kWarps;
-                if (j < closed) write_weight(a, w.bh, j, sm.total);
+            constexpr int kOnce = kThreads / kWeightLanes;
+            for (int e0 = 0; (e0 / kWarps) * step + rank * kWarps < closed; e0 += kOnce) {
+                const int e = e0 + tid / kWeightLanes, j = (e / kWarps) * step + rank * kWarps + e % kWarps;
+                write_weight(a, w.bh, j < closed ? j : -1, sm.total);
             }
         }
         if (a.cluster > 1) cluster.sync();  // the CTAs keep their shared memory until it has been read
@@ -981,7 +998,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 }
 
 // The blocks' weights where a key head's rows are joined from runs.
-// blockIdx.x: key head; blockIdx.y: 256 blocks at a time.
+// blockIdx.x: key head; blockIdx.y: kWeightBlocks blocks at a time.
+constexpr int kWeightBlocks = 2 * kJoinThreads / kWeightLanes;
 template <int NT>
 __global__ void __launch_bounds__(kJoinThreads) weight_kernel(const __grid_constant__ DecodeArgs a) {
     constexpr int kRows = 8 * NT;
@@ -990,9 +1008,10 @@ __global__ void __launch_bounds__(kJoinThreads) weight_kernel(const __grid_const
     const long long bh = blockIdx.x;
     int L = a.lens[bh / a.c.H];
     if (L < 0 || L / kBlock > a.c.blocks) L = 0;  // recorded by the attention
-    const int j = (int)blockIdx.y * kJoinThreads + threadIdx.x;
-    // (a key head's row tiles follow one another, so its rows do too)
-    if (j < L / kBlock) write_weight(a, bh, j, a.part.total + bh * a.tiles * kRows);
+    const int closed = L / kBlock, j0 = (int)blockIdx.y * kWeightBlocks;
+    for (int j = j0 + threadIdx.x / kWeightLanes; j < j0 + kWeightBlocks; j += kWeightBlocks / 2)
+        // (a key head's row tiles follow one another, so its rows do too)
+        write_weight(a, bh, j < closed ? j : -1, a.part.total + bh * a.tiles * kRows);
 }
 
 constexpr int kSms = 148;
@@ -1116,7 +1135,7 @@ cudaError_t launch(const DecodeArgs &a, const Plan &p, cudaStream_t st, LaunchIn
         li.kernels += 1;
     }
     if (a.weight && !a.weigh) {
-        const dim3 g((unsigned)(a.c.B * a.c.H), (unsigned)((a.c.blocks + kJoinThreads - 1) / kJoinThreads));
+        const dim3 g((unsigned)(a.c.B * a.c.H), (unsigned)((a.c.blocks + kWeightBlocks - 1) / kWeightBlocks));
         if ((e = launch_pdl(weight_kernel<NT>, g, dim3(kJoinThreads), 0, st, a)) != cudaSuccess)
             return e;
         li.kernels += 1;
