@@ -110,8 +110,8 @@ struct Cfg {
 struct Parts {
     float *o;    // [run + tile][rows][D]
     float2 *ml;  // [run + tile][rows]
-    float *total;  // [tile][rows] log2 of each row's sum (with weights)
-    float *lb;   // [B * Hkv][blocks][R]
+    float *total;  // [tile][rows] log2 of each row's sum, for the kernel that writes the weights, or NULL
+    float *lb;     // [B * Hkv][blocks][R]
 };
 
 template <int D, int NT>
@@ -149,6 +149,7 @@ struct DecodeArgs {
     int H, G, Tq;   // query heads, heads of a group, new tokens
     int rows;       // rows of a group: G * Tq, or G with lists (a group is then one token)
     int tiles;      // row tiles of a group
+    int tile_rows;  // rows of a tile
     int cluster;    // CTAs of a cluster, which share a row tile; 0: no clusters, but
     int runs;       // this many runs
     bool weigh;     // the decode kernel writes the blocks' weights
@@ -450,6 +451,9 @@ __device__ __forceinline__ void join(float4 &o, float &l, float f, float l1, con
     o.w = fmaf(f, o1.w, o.w);
 }
 
+// log2 of a row's sum, in the units of the blocks' sums; a row that sees nothing gives nothing.
+__device__ __forceinline__ float row_total(float m, float l) { return l == 0.f ? INFINITY : m + lg2(l); }
+
 // Four channels of row `r` of a group, and with the first ones its lse.
 __device__ __forceinline__ void write_row(const DecodeArgs &a, const Where &w, int r, int ch, float m, float l,
                                           const float4 &o) {
@@ -458,12 +462,11 @@ __device__ __forceinline__ void write_row(const DecodeArgs &a, const Where &w, i
     *reinterpret_cast<uint2 *>(a.o + (long long)w.b * a.so.b + (long long)head * a.so.h + (long long)tok * a.so.t +
                                ch) =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (ch == 0)
+    if (ch == 0) {
         a.lse[((long long)w.b * a.H + head) * a.Tq + tok] = l == 0.f ? -INFINITY : (m + (log2f(l) - kPShift)) * kLn2;
+        if (a.part.total) a.part.total[w.bh * (a.tiles * a.tile_rows) + r] = row_total(m, l);
+    }
 }
-
-// log2 of a row's sum, in the units of the blocks' sums; a row that sees nothing gives nothing.
-__device__ __forceinline__ float row_total(float m, float l) { return l == 0.f ? INFINITY : m + log2f(l); }
 
 // weight[j] (+)= sum over the rows of exp(block j's log-sum - the row's log-sum),
 // by eight consecutive lanes a block (all lanes of a warp call it; j < 0: none).
@@ -993,16 +996,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 #pragma unroll
         for (int y = 1; y < kParts; ++y) join(o, l, 1.f, sl[y], so[y][tid]);
         write_row(a, w, w.tile * kRows + row, 4 * tid, m, l, o);
-        if (tid == 0 && a.weight) a.part.total[(long long)group * kRows + row] = row_total(m, l);
     }
 }
 
-// The blocks' weights where a key head's rows are joined from runs.
+// The blocks' weights where a key head's rows are joined from runs, or lie in
+// several row tiles.
 // blockIdx.x: key head; blockIdx.y: kWeightBlocks blocks at a time.
 constexpr int kWeightBlocks = 2 * kJoinThreads / kWeightLanes;
-template <int NT>
 __global__ void __launch_bounds__(kJoinThreads) weight_kernel(const __grid_constant__ DecodeArgs a) {
-    constexpr int kRows = 8 * NT;
     grid_dep_wait();
     grid_dep_launch();
     const long long bh = blockIdx.x;
@@ -1011,10 +1012,9 @@ __global__ void __launch_bounds__(kJoinThreads) weight_kernel(const __grid_const
     const int closed = L / kBlock, j0 = (int)blockIdx.y * kWeightBlocks;
     for (int j = j0 + threadIdx.x / kWeightLanes; j < j0 + kWeightBlocks; j += kWeightBlocks / 2)
         // (a key head's row tiles follow one another, so its rows do too)
-        write_weight(a, bh, j < closed ? j : -1, a.part.total + bh * a.tiles * kRows);
+        write_weight(a, bh, j < closed ? j : -1, a.part.total + bh * (a.tiles * a.tile_rows));
 }
 
-constexpr int kSms = 148;
 // CTAs that the GPU holds at once in clusters of 1 .. 8, with up to 1, 2 and 3
 // CTAs an SM (cudaOccupancyMaxActiveClusters on B200: a cluster lies within a
 // part of the GPU, and the parts' sizes leave SMs over).
@@ -1076,16 +1076,13 @@ Plan make_plan(const Q8Cache &c, int H, int Tq, int list_n, bool weight) {
     p.tiles = (p.rows + 8 * p.nt - 1) / (8 * p.nt);
     p.groups = (long long)c.B * c.H * (lists ? Tq : 1) * p.tiles;
     p.shares = shares_for(p.groups, p.nt, lists && list_n < c.blocks ? list_n : c.blocks);
-    // a key head's rows in several tiles: the weights are summed by a kernel that finds their sums in the workspace
-    if (weight && p.shares.cluster && p.tiles > 1)
-        p.shares = Shares{0, kSms};
-    p.weigh = weight && p.shares.cluster;
+    p.weigh = weight && p.shares.cluster && p.tiles == 1;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     const size_t rows = p.shares.cluster ? 0 : (size_t)(p.groups + p.shares.runs) * 8 * p.nt;
     p.o = 0;
     p.ml = up(rows * c.D * sizeof(float));
     p.total = p.ml + up(rows * sizeof(float2));
-    p.lb = p.total + (weight && rows ? up((size_t)p.groups * 8 * p.nt * sizeof(float)) : 0);
+    p.lb = p.total + (weight && !p.weigh ? up((size_t)p.groups * 8 * p.nt * sizeof(float)) : 0);
     p.bytes = p.lb + (weight ? up((size_t)c.B * c.H * p.rows * c.blocks * sizeof(float)) : 0);
     return p;
 }
@@ -1136,7 +1133,7 @@ cudaError_t launch(const DecodeArgs &a, const Plan &p, cudaStream_t st, LaunchIn
     }
     if (a.weight && !a.weigh) {
         const dim3 g((unsigned)(a.c.B * a.c.H), (unsigned)((a.c.blocks + kWeightBlocks - 1) / kWeightBlocks));
-        if ((e = launch_pdl(weight_kernel<NT>, g, dim3(kJoinThreads), 0, st, a)) != cudaSuccess)
+        if ((e = launch_pdl(weight_kernel, g, dim3(kJoinThreads), 0, st, a)) != cudaSuccess)
             return e;
         li.kernels += 1;
     }
@@ -1166,6 +1163,7 @@ cudaError_t q8_decode(const Q8Cache &c, const Q8Decode &d, int *err, cudaStream_
     a.Tq = d.Tq;
     a.rows = p.rows;
     a.tiles = p.tiles;
+    a.tile_rows = 8 * p.nt;
     a.cluster = p.shares.cluster;
     a.runs = p.shares.runs;
     a.weigh = p.weigh;
@@ -1174,7 +1172,7 @@ cudaError_t q8_decode(const Q8Cache &c, const Q8Decode &d, int *err, cudaStream_
     char *ws = static_cast<char *>(d.workspace);
     a.part.o = reinterpret_cast<float *>(ws + p.o);
     a.part.ml = reinterpret_cast<float2 *>(ws + p.ml);
-    a.part.total = reinterpret_cast<float *>(ws + p.total);
+    a.part.total = d.weight && !p.weigh ? reinterpret_cast<float *>(ws + p.total) : nullptr;
     a.part.lb = reinterpret_cast<float *>(ws + p.lb);
     a.err = err;
 #define ATTN_Q8_CASE(DD, NN) \
