@@ -90,14 +90,16 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return r;
 }
 // Warps of a CTA, slots of a warp's ring (a block, or half of one at D = 128),
-// and CTAs that an SM holds: 168 registers a thread for up to 8 rows, 255 for 16.
+// and CTAs that an SM holds: three of 168 registers a thread, or two of 255 where
+// the sums take more (16 rows of 64 channels with three CTAs, spilling 36 bytes,
+// against two: 21.9 and 34.2 us on 432 row tiles, 14.4 and 13.7 on 6).
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 template <int D, int NT>
 struct Cfg {
-    static constexpr int kCtas = NT == 1 ? 3 : 2;
+    static constexpr int kCtas = NT == 1 || (NT == 2 && D < 128) ? 3 : 2;
     static constexpr int kHalves = D == 128 ? 2 : 1;  // slots of a block
-    static constexpr int kSlots = D == 32 ? 4 : (NT == 1 ? 2 : 3);
+    static constexpr int kSlots = D == 32 ? 4 : (kCtas == 3 ? 2 : 3);
     static constexpr bool kQueriesInSmem = NT > 1;  // else in registers
     // tiles of 16 tokens (keys) or 16 channels (values) whose sums a warp forms side by side
     static constexpr int kAtOnce = NT == 4 ? 1 : D == 32 ? 2 : 4 / NT;
@@ -1021,10 +1023,10 @@ __global__ void __launch_bounds__(kJoinThreads) weight_kernel(const __grid_const
 constexpr int kRoom[3][kMaxCluster] = {{148, 148, 135, 132, 130, 132, 105, 120},
                                        {296, 296, 279, 284, 280, 270, 259, 264},
                                        {444, 444, 426, 416, 410, 426, 392, 384}};
-constexpr int ctas_of(int nt) { return nt == 1 ? Cfg<64, 1>::kCtas : Cfg<64, 2>::kCtas; }  // (2 and 4 alike)
-static_assert(Cfg<32, 1>::kCtas == Cfg<64, 1>::kCtas && Cfg<128, 1>::kCtas == Cfg<64, 1>::kCtas &&
-                  Cfg<32, 2>::kCtas == Cfg<64, 2>::kCtas && Cfg<128, 2>::kCtas == Cfg<64, 2>::kCtas,
-              "CTAs an SM holds do not depend on the head size");
+template <int D>
+constexpr int ctas_on_sm(int nt) {
+    return nt == 1 ? Cfg<D, 1>::kCtas : nt == 2 ? Cfg<D, 2>::kCtas : Cfg<D, 4>::kCtas;
+}
 
 // Clusters (the CTAs of one, 0: none) or runs, by what each costs in the time a
 // warp takes for a block, as if every sequence filled its cache.  Clusters of n
@@ -1042,8 +1044,9 @@ constexpr int kLongRun = 100;
 struct Shares {
     int cluster, runs;
 };
-Shares shares_for(long long tiles, int nt, int blocks) {
-    const int(&held)[kMaxCluster] = kRoom[ctas_of(nt) - 1];
+Shares shares_for(long long tiles, int D, int nt, int blocks) {
+    const int on_sm = D == 32 ? ctas_on_sm<32>(nt) : D == 64 ? ctas_on_sm<64>(nt) : ctas_on_sm<128>(nt);
+    const int(&held)[kMaxCluster] = kRoom[on_sm - 1];
     int best = 1;
     long long least = 0;
     for (int n = 1; n <= kMaxCluster; ++n) {
@@ -1075,7 +1078,7 @@ Plan make_plan(const Q8Cache &c, int H, int Tq, int list_n, bool weight) {
     p.nt = p.rows > 16 && c.D < 128 ? 4 : p.rows > 8 ? 2 : 1;
     p.tiles = (p.rows + 8 * p.nt - 1) / (8 * p.nt);
     p.groups = (long long)c.B * c.H * (lists ? Tq : 1) * p.tiles;
-    p.shares = shares_for(p.groups, p.nt, lists && list_n < c.blocks ? list_n : c.blocks);
+    p.shares = shares_for(p.groups, c.D, p.nt, lists && list_n < c.blocks ? list_n : c.blocks);
     p.weigh = weight && p.shares.cluster && p.tiles == 1;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     const size_t rows = p.shares.cluster ? 0 : (size_t)(p.groups + p.shares.runs) * 8 * p.nt;
