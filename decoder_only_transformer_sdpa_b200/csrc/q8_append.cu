@@ -74,9 +74,9 @@ __global__ void __launch_bounds__(kThreads)
     const int b = (int)(bh / c.H), h = (int)(bh % c.H);
     grid_dep_wait();
     grid_dep_launch();
-    const int L = checked_length(lens, b, c.blocks, err);
+    const int length = lens[b], m = new_lens ? new_lens[b] : n;
+    const int L = checked_length(length, c.blocks, err);
     if (L < 0) return;
-    int m = new_lens ? new_lens[b] : n;
     if (m < 0 || m > n || m > L) {
         if (tid == 0) atomicExch(err, kErrLength);
         return;
@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(kReadThreads)
     const int b = (int)(bh / c.H);
     grid_dep_wait();
     grid_dep_launch();
-    int L = checked_length(lens, b, c.blocks, err);
-    int start = starts ? starts[b] : 0;
+    const int length = lens[b];
+    int start = starts ? starts[b] : 0, L = checked_length(length, c.blocks, err);
     if (start < 0) {
         if (tid == 0) atomicExch(err, kErrLength);
         L = -1;

@@ -41,10 +41,9 @@ __device__ __forceinline__ int key_offset(int t, int ch) {
     return (ch / S) * (kBlock * S) + t * S + ch % S;
 }
 
-// The length of sequence b, or -1 (recorded in the error word) when it is
-// negative or beyond what the cache holds.
-__device__ __forceinline__ int checked_length(const int32_t *lens, int b, int blocks, int *err) {
-    const int L = lens[b];
+// A sequence's length L, or -1 (recorded in the error word) when it is negative
+// or beyond what the cache holds.
+__device__ __forceinline__ int checked_length(int L, int blocks, int *err) {
     if (L < 0 || L / kBlock > blocks) {
         if (threadIdx.x == 0) atomicExch(err, kErrLength);
         return -1;

@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
                 load_row<D, true>(qx[nt], qrow[nt], t);
             }
         }
-        int L = checked_length(a.lens, w.b, a.c.blocks, a.err);
+        int L = checked_length(a.lens[w.b], a.c.blocks, a.err);
         if (L < 0) L = 0;
         // ---- this warp's blocks: places first, first + step, ... below `count` (of all closed blocks, or of the list),
         // and its tokens of the open block: open_at, + 16 step, ... below `open`
@@ -968,7 +968,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     const Where w = where(a, group);
     if (w.tile * kRows + row >= a.rows) return;
     // The lengths are there: the attention, which does not write them, waited for what came before it.
-    checked_length(a.lens, w.b, a.c.blocks, a.err);  // (a sequence without units is in no run)
+    checked_length(a.lens[w.b], a.c.blocks, a.err);  // (a sequence without units is in no run)
     int first, last;
     runs_of_tile(a, group, first, last);
     grid_dep_wait();

@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads)
     };
     const int step = kRow * kAtOnce;
     load(rank * step, c.blocks);
-    const int L = max(0, checked_length(lens, b, c.blocks, err));
+    const int L = max(0, checked_length(lens[b], c.blocks, err));
     const int last = L - Tq + r;  // the query's own position
     const int count = last < 0 ? 0 : min(L / kBlock, last / kBlock + 1);
     if (count > n) {  // (the same in all CTAs of the cluster)
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads)
     const int b = (int)(bh / c.H);
     grid_dep_wait();
     grid_dep_launch();
-    const int L = checked_length(lens, b, c.blocks, err);
+    const int L = checked_length(lens[b], c.blocks, err);
     const int closed = L < 0 ? 0 : L / kBlock;
     const float *weight = c.weight + bh * c.blocks;
     if (closed > keep) {

@@ -379,8 +379,8 @@ size_t attn_q8_decode_workspace_bytes(const attn_q8_cache *cache, int H, int Tq,
  * lens[b] - Tq + r; where that is below zero nothing is seen: o = 0, lse =
  * -inf.  workspace: at least attn_q8_decode_workspace_bytes bytes, 256-byte
  * aligned, its contents do not matter (NULL where that is 0).  One launch;
- * one more to join the parts of few heads over many blocks, and one for the
- * weights of such heads and of more than 16 rows. */
+ * a second one joins the parts of few heads over many blocks, and another sums
+ * the weights of those and of more than 16 rows (32 at D 32 and 64). */
 int attn_q8_decode(const attn_q8_cache *cache, const void *q, void *o, float *lse,
                    const int32_t *lens, int H, int Tq, float scale, const attn_strides *strides,
                    const attn_q8_decode_options *opts, void *workspace, size_t workspace_bytes,
@@ -449,8 +449,8 @@ int attn_bwd_f32_ex(const float *q, const float *k, const float *v, const float 
 
 /* Synchronises `stream`, then reads and clears the current device's
  * in-kernel error flag.  Returns ATTN_OK, ATTN_ERR_TIMEOUT (a bounded wait
- * ran out since the last call), ATTN_ERR_LENGTH (a length or block list of an
- * 8-bit cache's call was out of range), ATTN_ERR_DEVICE_CHECK (the debug build
+ * ran out since the last call), ATTN_ERR_LENGTH (a length or block list of a
+ * call on an 8-bit cache was out of range), ATTN_ERR_DEVICE_CHECK (the debug build
  * libattn_debug.so only: a kernel's bounds check on a tile coordinate, TMEM
  * column or shared-memory offset failed; the kernel records it and carries
  * on) or ATTN_ERR_CUDA (the sync itself failed, or a kernel found its dynamic
@@ -476,9 +476,10 @@ int attn_selftest_device_check(cudaStream_t stream);
  * enqueued (for launch accounting). */
 int attn_last_launch_count(void);
 
-/* Timing hook: arms the next forward or backward call made on this host
- * thread to record `start` just before and `end` just after enqueueing its
- * main kernel (the forward kernel, or the backward's tile kernel), on the
+/* Timing hook: arms the next forward, backward, decode or attn_q8_* call made
+ * on this host thread to record `start` just before and `end` just after
+ * enqueueing its main kernel (the forward kernel, the backward's tile kernel,
+ * the decode kernel, the kernel that moves an eviction's blocks), on the
  * call's stream.  Both are cudaEvent_t handles owned by the caller; the call
  * consumes the arming whether or not it succeeds.  Pass NULLs to disarm. */
 typedef struct CUevent_st *cudaEvent_t;
