@@ -1034,8 +1034,9 @@ constexpr int ctas_on_sm(int nt) {
 // a warp reads and kPerCta beside them.  Runs: each warp's even share of all units
 // and kPerRuns for finding them and joining what they leave.  Measured (us,
 // clusters / runs; row tiles x blocks): 144 x 16 7.9 / 9.6, 200 x 64 22 / 23,
-// 32 x 257 (head size 128, 16 rows) 33 / 37, 432 x 24 (16 rows) 34 / 46, 6 x 265
-// (16 rows) 17 / 14.5, 1 x 2048 66 / 22, 192 x up to 512 98 / 84.
+// 32 x 257 (head size 128, 16 rows) 33 / 37, 432 x 24 (16 rows) 22 / 46, 6 x 265
+// (16 rows) 17 / 14.5, 1 x 2048 66 / 22, 192 x up to 512 98 / 84.  Runs where the
+// two come out alike: unequal lengths, which they even out, cost clusters more.
 constexpr int kPerCta = 3, kPerRuns = 5;
 // Where a run is long, two for each CTA that the GPU holds let an SM that is
 // quicker than others take more of them (83.9 us against 85.2 at 230 units a run;
@@ -1059,7 +1060,7 @@ Shares shares_for(long long tiles, int D, int nt, int blocks) {
         }
     }
     const long long units = tiles * (blocks + kPad + kOpen), each = units / held[0];
-    if (units < (1ll << 31) && each / kWarps + 1 + kPerRuns < least) return Shares{0, held[0] * (each >= kLongRun ? 2 : 1)};
+    if (units < (1ll << 31) && each / kWarps + 1 + kPerRuns <= least) return Shares{0, held[0] * (each >= kLongRun ? 2 : 1)};
     return Shares{best, 0};
 }
 
