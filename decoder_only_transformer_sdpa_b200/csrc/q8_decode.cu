@@ -897,6 +897,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
             do {
                 if (++group >= (unsigned)a.c.B * tiles_of_sequence(a)) return;
             } while (units_of(a, where(a, group).b) == 0);
+            fence_proxy_async_smem();
             __syncthreads();  // the rings take blocks again
             continue;
         }
@@ -1079,7 +1080,7 @@ Plan make_plan(const Q8Cache &c, int H, int Tq, int list_n, bool weight) {
     p.nt = p.rows > 16 && c.D < 128 ? 4 : p.rows > 8 ? 2 : 1;
     p.tiles = (p.rows + 8 * p.nt - 1) / (8 * p.nt);
     p.groups = (long long)c.B * c.H * (lists ? Tq : 1) * p.tiles;
-    p.shares = shares_for(p.groups, c.D, p.nt, lists && list_n < c.blocks ? list_n : c.blocks);
+    p.shares = shares_for(p.groups, c.D, p.nt, lists ? list_n : c.blocks);  // (the kernel counts a list's places too)
     p.weigh = weight && p.shares.cluster && p.tiles == 1;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     const size_t rows = p.shares.cluster ? 0 : (size_t)(p.groups + p.shares.runs) * 8 * p.nt;

@@ -168,6 +168,13 @@ def test_workspace_sizes():
     assert A.lib().attn_q8_evict_workspace_bytes(ctypes.byref(cache(H=0))) == 0
 
 
+def test_long_lists_of_many_row_tiles_are_counted_as_the_kernel_counts_them():
+    """131072 row tiles of 32768 places each are more units than runs are made of, however few blocks the cache has."""
+    many = cache(B=4096, H=32, blocks=1, D=32)
+    opts = lambda n: ctypes.byref(A.attn_q8_decode_options(None, n, 0))
+    assert A.lib().attn_q8_decode_workspace_bytes(ctypes.byref(many), 32, 1, opts(32768)) == 0
+
+
 def test_status_string():
     assert A.attn_status_string(E_LENGTH) != A.attn_status_string(12345)
 
