@@ -13,6 +13,11 @@ namespace {
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+bool overlap(const void *a, size_t an, const void *b, size_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + bn && y < x + an;
+}
+
 bool strides_ok(const attn_strides &x) {
     auto ok = [](int64_t v) { return v > 0 && v % 8 == 0 && v < (1ll << 39); };
     return ok(x.b) && ok(x.h) && ok(x.t);
@@ -201,7 +206,16 @@ ATTN_API int attn_q8_evict(const attn_q8_cache *cache, const attn_q8_cache *out,
     for (bool s : same)
         if (s != same[0]) return ATTN_ERR_OPTION;
     if (same[0] && (c.blocks != d.blocks || c.bounds != d.bounds)) return ATTN_ERR_OPTION;
-    if (!same[0] && c.bounds && c.bounds == d.bounds) return ATTN_ERR_OPTION;
+    if (!same[0]) {
+        const size_t blocks = (size_t)c.B * c.H * c.blocks, to = (size_t)d.B * d.H * d.blocks, side = (size_t)kQ8Block * c.D;
+        const size_t ring = (size_t)c.B * c.H * 2 * side * sizeof(__nv_bfloat16);
+        if (overlap(c.k_codes, blocks * side, d.k_codes, to * side) ||
+            overlap(c.v_codes, blocks * side, d.v_codes, to * side) ||
+            overlap(c.scales, blocks * 8, d.scales, to * 8) || overlap(c.recent_k, ring, d.recent_k, ring) ||
+            overlap(c.recent_v, ring, d.recent_v, ring) || (d.weight && overlap(c.weight, blocks * 4, d.weight, to * 4)) ||
+            (d.bounds && overlap(c.bounds, blocks * 2 * c.D, d.bounds, to * 2 * c.D)))
+            return ATTN_ERR_OPTION;
+    }
     if (!aligned(lens, 4) || !aligned(lens_out, 4) || !aligned(kept, 4)) return ATTN_ERR_ALIGN;
     if (lens_out == lens &&
         (!workspace || workspace_bytes < attn_q8_evict_workspace_bytes(cache) || !aligned(workspace, 256)))

@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kMoveThreads)
     const int count = fate.kept;
     const int32_t *from = kept + bh * keep;
     // this chunk's blocks: all of them when they move within one cache
-    const int per = (keep + chunks - 1) / chunks;
+    const int per = (min(keep, c.blocks) + chunks - 1) / chunks;
     const int begin = chunk * per, end = min(count, begin + per);
     ATTN_DCHECK(count <= d.blocks && count <= keep && (!same || chunks == 1), err);
     if (slice < kSlices) {
@@ -459,7 +459,8 @@ cudaError_t q8_evict(const Q8Cache &src, const Q8Cache &dst, const int32_t *lens
     const int slices = 2 * kQ8Block * src.D / kSlice + 1;
     // Within one cache a head's blocks move in one run; into another one they
     // are cut into chunks of 32, a round of a CTA's loads.
-    const int chunks = src.k_codes == dst.k_codes ? 1 : (keep + kAtOnce * kRounds - 1) / (kAtOnce * kRounds);
+    const int most = keep < src.blocks ? keep : src.blocks;
+    const int chunks = src.k_codes == dst.k_codes ? 1 : (most + kAtOnce * kRounds - 1) / (kAtOnce * kRounds);
     const long long grid = heads * slices * chunks;
     if (heads > 0x7fffffffLL || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     if ((e = launch_pdl(keep_kernel, dim3((unsigned)heads), dim3(kThreads), (size_t)src.blocks * 4, st, src, lens, kept,

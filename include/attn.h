@@ -414,8 +414,11 @@ size_t attn_q8_evict_workspace_bytes(const attn_q8_cache *cache);
  * blocks.  lens_out [B] (may be lens) gets the new lengths: min(closed, keep)
  * * 64 + lens[b] % 64; kept int32 [B, H, keep] the places the blocks came from,
  * ascending, -1 behind the last.  Heads keep different blocks, all of them
- * equally many.  workspace: as attn_q8_evict_workspace_bytes, 256-byte
- * aligned, where lens_out is lens; else it is not looked at.  Two launches. */
+ * equally many.  The bf16 positions go along unchanged: where the last block
+ * does not stay in every head (recent 0), lens may not fall into it, nor an
+ * append before it be repeated, until 64 tokens more are there.  workspace: as
+ * attn_q8_evict_workspace_bytes, 256-byte aligned, where lens_out is lens; else
+ * it is not looked at.  Two launches. */
 int attn_q8_evict(const attn_q8_cache *cache, const attn_q8_cache *out, const int32_t *lens,
                   int32_t *lens_out, int32_t *kept, int keep, int sink, int recent, void *workspace,
                   size_t workspace_bytes, cudaStream_t stream);

@@ -141,6 +141,10 @@ OTHER = dict(k_codes=11 * P, v_codes=12 * P, scales=13 * P, bounds=14 * P, weigh
     (dict(out=cache(**{**OTHER, "k_codes": P})), E_OPTION), (dict(out=cache(**{**OTHER, "scales": 3 * P})), E_OPTION),
     (dict(out=cache(**{**OTHER, "recent_v": 7 * P})), E_OPTION), (dict(out=cache(**{**OTHER, "bounds": 4 * P})), E_OPTION),
     (dict(out=cache(**{**OTHER, "weight": 5 * P})), E_OPTION), (dict(out=cache(blocks=3)), E_OPTION),
+    (dict(out=cache(**{**OTHER, "k_codes": P + 64})), E_OPTION), (dict(out=cache(**{**OTHER, "v_codes": 2 * P - 64})), E_OPTION),
+    (dict(out=cache(**{**OTHER, "scales": 3 * P + 8})), E_OPTION), (dict(out=cache(**{**OTHER, "bounds": 4 * P + 16})), E_OPTION),
+    (dict(out=cache(**{**OTHER, "weight": 5 * P - 4})), E_OPTION), (dict(out=cache(**{**OTHER, "recent_k": 6 * P + 256})), E_OPTION),
+    (dict(out=cache(**{**OTHER, "recent_v": 7 * P - 16})), E_OPTION),
     (dict(out=cache(bounds=None)), E_OPTION), (dict(lens_out=P + 2), E_ALIGN), (dict(kept=P + 2), E_ALIGN),
     # (lens_out is lens: only then is there a workspace)
     (dict(ws=None), E_WS), (dict(ws=P + 128), E_WS), (dict(ws_bytes=40), E_WS),

@@ -839,6 +839,23 @@ def test_other_streams_and_two_caches_at_once():
         check_decode(q.cpu(), *got[i], sequences(k, v, (n, n // 2)), (n, n // 2))
 
 
+def test_evict_into_a_cache_without_bounds_and_weight():
+    n = 64 * 9 + 20
+    k, v = tokens(88, 1, 2, n, 32)
+    c, L = filled(k, v, (n,))
+    c.weight.copy_(torch.rand(1, 2, c.blocks, generator=torch.Generator().manual_seed(1)))
+    room = A.Q8Cache.empty(1, 2, 32, n, device=dev(), bounds=False, weight=False)
+    after, kept = A.attn_q8_evict(c, L, 30000, sink=1, out=room)  # (more than there are: a copy)
+    assert status() == 0 and after.tolist() == [n] and (kept[:, :, 9:] == -1).all()
+    q = queries(13, 1, 2, 1, 32).to(dev())
+    for x, y in zip(A.attn_q8_decode(q, room, after), A.attn_q8_decode(q, c, L)):
+        assert torch.equal(x, y)
+    after, kept = A.attn_q8_evict(c, L, 4, sink=1, out=room)
+    assert status() == 0 and after.tolist() == [4 * 64 + 20]
+    for h in range(2):
+        assert torch.equal(room.k_codes[0, h, :4], c.k_codes[0, h, kept[0, h].long()])
+
+
 def test_results_do_not_depend_on_the_run():
     """The same call gives the same bits, with the workspace holding anything."""
     k, v = tokens(90, 2, 3, 2000, 128)
