@@ -641,22 +641,31 @@ def _view(t, name, dtype, shape, index):
     return p
 
 
-def _used_on(stream, index, *tensors):
-    """Tells the allocator that tensors made for this call are in use on a
-    stream other than the current one."""
-    if stream != _torch().cuda.current_stream(index):
-        for t in tensors:
-            t.record_stream(stream)
+def _on_stream(stream, fn, cache, *args):
+    """fn(*args) on `stream`: what it allocates comes from that stream's memory,
+    which no earlier work on the current stream still uses, and what it returns
+    stays allocated while the current stream, for the caller, uses it."""
+    cuda = _torch().cuda
+    index = _check_cache(cache)
+    if stream.device_index != index:
+        raise ValueError(f"stream must be on cuda:{index}, got cuda:{stream.device_index}")
+    current = cuda.current_stream(index)
+    with cuda.stream(stream):
+        results = fn(*args)
+    if stream != current and results is not None:
+        for t in results if isinstance(results, tuple) else (results,):
+            t.record_stream(current)
+    return results
 
 
-def _call(fn, where, index, stream, *args):
-    """The library call on device `index`, on `stream` (None: the current one of that device)."""
+def _call(fn, where, index, *args):
+    """The library call on device `index`, on its current stream."""
     C = _torch()._C
-    if stream is None and C._cuda_getDevice() == index:
+    if C._cuda_getDevice() == index:
         status = fn(*args, C._cuda_getCurrentRawStream(index))
     else:
         with _torch().cuda.device(index):
-            status = fn(*args, _stream_handle(stream))
+            status = fn(*args, C._cuda_getCurrentRawStream(index))
     if status != 0:
         raise AttnError(status, where)
 
@@ -666,6 +675,8 @@ def attn_q8_append(cache, k, v, lens, new_lens=None, stream=None) -> None:
     or strided views) into the cache.  ``lens`` [B] int32 counts them already;
     ``new_lens`` [B] int32: how many of the n rows are sequence b's (the first
     ones; None: all n)."""
+    if stream is not None:
+        return _on_stream(stream, attn_q8_append, cache, cache, k, v, lens, new_lens)
     index = _check_cache(cache)
     bf16, i32, _ = cache.types
     n = k.shape[2] if k.dim() == 4 else _shape4(k)
@@ -674,12 +685,14 @@ def attn_q8_append(cache, k, v, lens, new_lens=None, stream=None) -> None:
     lp = _whole(lens, "lens", i32, cache.batch, index)
     np_ = None if new_lens is None else _whole(new_lens, "new_lens", i32, cache.batch, index)
     st = None if k.is_contiguous() and v.is_contiguous() else _strides_of(k, v)
-    _call(_lib.attn_q8_append, "attn_q8_append", index, stream, cache.ref, kp, vp, n, lp, np_, st)
+    _call(_lib.attn_q8_append, "attn_q8_append", index, cache.ref, kp, vp, n, lp, np_, st)
 
 
 def attn_q8_read(cache, lens, n: int, starts=None, k=None, v=None, stream=None):
     """Positions starts[b] .. + n - 1 (None: from 0) as the cache holds them,
     in bf16 [B, H, n, D], zero past a sequence's end.  Returns (k, v)."""
+    if stream is not None:
+        return _on_stream(stream, attn_q8_read, cache, cache, lens, n, starts, k, v)
     index = _check_cache(cache)
     bf16, i32, _ = cache.types
     shape = (cache.B, cache.H, int(n), cache.D)
@@ -687,20 +700,17 @@ def attn_q8_read(cache, lens, n: int, starts=None, k=None, v=None, stream=None):
         raise AttnError(-2, "attn_q8_read")
     lp = _whole(lens, "lens", i32, cache.batch, index)
     sp = None if starts is None else _whole(starts, "starts", i32, cache.batch, index)
-    made = []
     if k is None:
-        made.append(k := cache.new(bf16, shape))
+        k = cache.new(bf16, shape)
         kp = k.data_ptr()
     else:
         kp = _whole(k, "k", bf16, shape, index)
     if v is None:
-        made.append(v := cache.new(bf16, shape))
+        v = cache.new(bf16, shape)
         vp = v.data_ptr()
     else:
         vp = _whole(v, "v", bf16, shape, index)
-    _call(_lib.attn_q8_read, "attn_q8_read", index, stream, cache.ref, lp, sp, int(n), kp, vp)
-    if stream is not None:
-        _used_on(stream, index, *made)
+    _call(_lib.attn_q8_read, "attn_q8_read", index, cache.ref, lp, sp, int(n), kp, vp)
     return k, v
 
 
@@ -720,6 +730,8 @@ def attn_q8_decode(q, cache, lens, o=None, lse=None, scale: Optional[float] = No
     blocks to attend to (the open one always is).  ``weight``: "set" or "add"
     to keep the attention weight of each closed block in cache.weight.
     Returns (O [B, Hq, Tq, D], lse [B, Hq, Tq])."""
+    if stream is not None:
+        return _on_stream(stream, attn_q8_decode, cache, q, cache, lens, o, lse, scale, blocks, weight, workspace)
     index = _check_cache(cache)
     bf16, i32, f32 = cache.types
     _, H, Tq, D = q.shape if q.dim() == 4 else _shape4(q)
@@ -730,14 +742,13 @@ def attn_q8_decode(q, cache, lens, o=None, lse=None, scale: Optional[float] = No
     qp = _view(q, "q", bf16, shape, index)
     lp = _whole(lens, "lens", i32, cache.batch, index)
     plain = q.is_contiguous()
-    made = []
     if o is None:
-        made.append(o := cache.new(bf16, shape))
+        o = cache.new(bf16, shape)
         op = o.data_ptr()
     else:
         op = _view(o, "o", bf16, shape, index)
     if lse is None:
-        made.append(lse := cache.new(f32, shape[:3]))
+        lse = cache.new(f32, shape[:3])
         ep = lse.data_ptr()
     else:
         ep = _whole(lse, "lse", f32, shape[:3], index)
@@ -755,15 +766,13 @@ def attn_q8_decode(q, cache, lens, o=None, lse=None, scale: Optional[float] = No
             need = int(_lib.attn_q8_decode_workspace_bytes(cache.ref, H, Tq, opts))
             cache.needs[(H, Tq, n, keep)] = need
         if need:
-            made.append(workspace := cache.k_codes.new_empty(need))
+            workspace = cache.k_codes.new_empty(need)
     elif not workspace.is_contiguous() or workspace.get_device() != index:
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
     wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     st = None if plain and o.is_contiguous() else _strides_of(q, o)
-    _call(_lib.attn_q8_decode, "attn_q8_decode", index, stream, cache.ref, qp, op, ep, lp, H, Tq,
+    _call(_lib.attn_q8_decode, "attn_q8_decode", index, cache.ref, qp, op, ep, lp, H, Tq,
           1.0 / math.sqrt(D) if scale is None else float(scale), st, opts, wp, wn)
-    if stream is not None:
-        _used_on(stream, index, *made)
     return o, lse
 
 
@@ -771,6 +780,8 @@ def attn_q8_select(q, cache, lens, n: int, blocks=None, stream=None):
     """The n closed blocks that each query of q (as in attn_q8_decode) is
     likely to attend to most, by a bound on their keys' products with it:
     int32 [B, H, Tq, n], ascending, -1 behind the last."""
+    if stream is not None:
+        return _on_stream(stream, attn_q8_select, cache, q, cache, lens, n, blocks)
     index = _check_cache(cache)
     bf16, i32, _ = cache.types
     _, H, Tq, _ = q.shape if q.dim() == 4 else _shape4(q)
@@ -779,16 +790,13 @@ def attn_q8_select(q, cache, lens, n: int, blocks=None, stream=None):
     shape = (cache.B, cache.H, Tq, int(n))
     qp = _view(q, "q", bf16, (cache.B, H, Tq, cache.D), index)
     lp = _whole(lens, "lens", i32, cache.batch, index)
-    made = []
     if blocks is None:
-        made.append(blocks := cache.new(i32, shape))
+        blocks = cache.new(i32, shape)
         bp = blocks.data_ptr()
     else:
         bp = _whole(blocks, "blocks", i32, shape, index)
     st = None if q.is_contiguous() else _strides_of(q)
-    _call(_lib.attn_q8_select, "attn_q8_select", index, stream, cache.ref, qp, lp, bp, int(n), H, Tq, st)
-    if stream is not None:
-        _used_on(stream, index, *made)
+    _call(_lib.attn_q8_select, "attn_q8_select", index, cache.ref, qp, lp, bp, int(n), H, Tq, st)
     return blocks
 
 
@@ -803,6 +811,8 @@ def attn_q8_evict(cache, lens, keep: int, sink: int = 0, recent: int = 1, out=No
     moved to the front of ``out`` (None: of the cache itself).  Returns
     (lens_out [B], kept [B, H, keep]: the places the blocks came from, -1
     behind the last)."""
+    if stream is not None:
+        return _on_stream(stream, attn_q8_evict, cache, cache, lens, keep, sink, recent, out, lens_out, kept, workspace)
     index = _check_cache(cache)
     i32 = cache.types[1]
     out = cache if out is None else out
@@ -811,27 +821,24 @@ def attn_q8_evict(cache, lens, keep: int, sink: int = 0, recent: int = 1, out=No
     if keep < 1:
         raise AttnError(-2, "attn_q8_evict")
     lp = _whole(lens, "lens", i32, cache.batch, index)
-    made = []
     if lens_out is None:
-        made.append(lens_out := cache.new(i32, cache.batch))
+        lens_out = cache.new(i32, cache.batch)
         op = lens_out.data_ptr()
     else:
         op = _whole(lens_out, "lens_out", i32, cache.batch, index)
     shape = (cache.B, cache.H, int(keep))
     if kept is None:
-        made.append(kept := cache.new(i32, shape))
+        kept = cache.new(i32, shape)
         kp = kept.data_ptr()
     else:
         kp = _whole(kept, "kept", i32, shape, index)
     wp, wn = None, 0
     if workspace is None and op == lp:  # the only case that needs one
-        made.append(workspace := cache.k_codes.new_empty(attn_q8_evict_workspace_bytes(cache)))
+        workspace = cache.k_codes.new_empty(attn_q8_evict_workspace_bytes(cache))
     if workspace is not None:
         if not workspace.is_contiguous() or workspace.get_device() != index:
             raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
         wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call(_lib.attn_q8_evict, "attn_q8_evict", index, stream, cache.ref, out.ref, lp, op, kp, int(keep), int(sink),
+    _call(_lib.attn_q8_evict, "attn_q8_evict", index, cache.ref, out.ref, lp, op, kp, int(keep), int(sink),
           int(recent), wp, wn)
-    if stream is not None:
-        _used_on(stream, index, *made)
     return lens_out, kept

@@ -839,6 +839,75 @@ def test_other_streams_and_two_caches_at_once():
         check_decode(q.cpu(), *got[i], sequences(k, v, (n, n // 2)), (n, n // 2))
 
 
+def test_every_call_on_a_stream_that_is_not_current():
+    """What a call on another stream allocates is not memory that work queued on the current stream still reads."""
+    B, H, D, n = 2, 4, 64, 700
+    k, v = tokens(85, B, H, n, D)
+    c, L = filled(k, v, (n, n - 200))
+    q = queries(9, B, H, 1, D).to(dev())
+    side = torch.cuda.Stream()
+    want = [*A.attn_q8_decode(q, c, L, weight="set"), A.attn_q8_select(q, c, L, 3), *A.attn_q8_read(c, L, n),
+            c.weight.clone()]
+    room = A.Q8Cache.empty(B, H, D, n, device=dev())
+    want += A.attn_q8_evict(c, L, 5, sink=1, recent=1, out=room)
+    torch.cuda.synchronize()
+    # memory of the results' sizes, read by queued work and given back: the allocator hands it to the current stream's calls
+    lent = [torch.ones_like(x) for x in want]
+    copies = [torch.zeros_like(x) for x in want]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    for to, x in zip(copies, lent):
+        to.copy_(x)
+    x = None
+    del lent
+    got = [*A.attn_q8_decode(q, c, L, weight="set", stream=side), A.attn_q8_select(q, c, L, 3, stream=side),
+           *A.attn_q8_read(c, L, n, stream=side)]
+    with torch.cuda.stream(side):
+        got.append(c.weight.clone())
+    got += A.attn_q8_evict(c, L, 5, sink=1, recent=1, out=room, stream=side)
+    assert A.attn_q8_append(c, k[:, :, :1].to(dev()), v[:, :, :1].to(dev()), L, ints(0, 0), stream=side) is None
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert status() == 0
+    assert all((x == 1).all() for x in copies)
+    closed = (n // 64, (n - 200) // 64)
+    for i, (x, y) in enumerate(zip(got, want)):
+        if i == 5:  # (what is not closed has no weight)
+            assert all(torch.equal(x[b, :, :closed[b]], y[b, :, :closed[b]]) for b in range(B))
+        else:
+            assert torch.equal(x, y), i
+
+
+def test_strided_queries_choose_as_contiguous_ones():
+    B, H, G, D, tq, n = 2, 2, 3, 64, 4, 64 * 11 + 9
+    k, v = tokens(86, B, H, n, D)
+    c, L = filled(k, v, (n, 300))
+    packed = queries(11, B, tq, H * G + 2, D).to(dev())  # [B, T, heads, D]
+    q = packed.transpose(1, 2)[:, 1:-1]
+    got = A.attn_q8_select(q, c, L, 2)
+    assert torch.equal(got, A.attn_q8_select(q.contiguous(), c, L, 2)) and status() == 0
+
+
+def test_launches_and_timing_hook():
+    """One launch a call where the interface says so, and events around the main kernel."""
+    k, v = tokens(87, 2, 2, 640, 64)
+    c, L = filled(k, v, (640, 100))
+    q = queries(12, 2, 2, 1, 64).to(dev())
+    events = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    for e in events:
+        e.record()  # (made before they are handed over)
+    one = ints(0, 0)
+    for call, launches in ((lambda: A.attn_q8_append(c, k[:, :, :1].to(dev()), v[:, :, :1].to(dev()), L, one), 1),
+                           (lambda: A.attn_q8_read(c, L, 640), 1), (lambda: A.attn_q8_select(q, c, L, 2), 1),
+                           (lambda: A.attn_q8_decode(q, c, L, weight="set"), 1), (lambda: A.attn_q8_evict(c, L, 3), 2)):
+        A.attn_profile_next_call(*events)
+        call()
+        assert A.lib().attn_last_launch_count() == launches
+        torch.cuda.synchronize()
+        assert 0 < events[0].elapsed_time(events[1]) < 1000
+    assert status() == 0
+
+
 def test_evict_into_a_cache_without_bounds_and_weight():
     n = 64 * 9 + 20
     k, v = tokens(88, 1, 2, n, 32)
