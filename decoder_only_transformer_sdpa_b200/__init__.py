@@ -13,6 +13,7 @@ outputs may be passed in or are allocated.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 import os
 from typing import Optional
@@ -28,6 +29,10 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(
         f"{LIB_PATH} is not built; run `python decoder_only_transformer_sdpa_b200/build.py` "
         "(nvcc, sm_100a). There is no fallback implementation.")
+
+if not os.path.exists(os.path.join(_HERE, "_q8.so")):
+    raise ImportError(
+        f"{os.path.join(_HERE, '_q8.so')} is not built; run `python decoder_only_transformer_sdpa_b200/build.py`.")
 
 _lib = ctypes.CDLL(LIB_PATH)
 
@@ -541,6 +546,24 @@ def attn_decode(q, k, v, o=None, lse=None, scale: Optional[float] = None, stream
     return o, lse
 
 
+_q8 = None
+
+
+def _binding():
+    """The module that takes the 8-bit cache's calls on torch tensors to
+    libattn.so (csrc/q8_binding.cpp), loaded with the first cache: it links to
+    torch, which this package does not import before it is used."""
+    global _q8
+    if _q8 is None:
+        _torch()
+        module = importlib.import_module("._q8", __name__)
+        module.bind(AttnError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            _lib.attn_q8_append, _lib.attn_q8_read, _lib.attn_q8_decode_workspace_bytes, _lib.attn_q8_decode,
+            _lib.attn_q8_select, _lib.attn_q8_evict_workspace_bytes, _lib.attn_q8_evict)))
+        _q8 = module
+    return _q8
+
+
 class Q8Cache:
     """A cache of keys and values in 8 bits, by blocks of 64 tokens (layout and
     rules: include/attn.h): the tensors, and the structure the library takes.
@@ -551,7 +574,7 @@ class Q8Cache:
     Sequence lengths are the caller's: an int32 CUDA tensor ``lens`` [B] that
     counts the new tokens before they are appended."""
     __slots__ = ("k_codes", "v_codes", "scales", "bounds", "weight", "recent_k", "recent_v", "B", "H",
-                 "blocks", "D", "device", "index", "struct", "ref", "needs", "batch", "types", "blanks")
+                 "blocks", "D", "device", "struct", "native")
 
     def __init__(self, k_codes, v_codes, scales, bounds, weight, recent_k, recent_v):
         torch = _torch()
@@ -575,22 +598,7 @@ class Q8Cache:
         if any(t is not None and t.device != self.device for t in parts):
             raise ValueError("the cache's tensors must be on one device")
         self.struct = attn_q8_cache(*(None if t is None else t.data_ptr() for t in parts), B, H, blocks, D)
-        self.ref = ctypes.byref(self.struct)
-        self.index = self.device.index
-        self.needs = {}  # workspace bytes by (query heads, new tokens, list length, weights)
-        self.batch, self.types = (B,), (torch.bfloat16, torch.int32, torch.float32)
-        self.blanks = {}  # one-element tensors that stand for the outputs' types and shapes
-
-    def new(self, dtype, shape):
-        """A new contiguous tensor on the cache's device.  (empty_like of an
-        expanded one-element tensor costs the host half of new_empty.)"""
-        torch = _torch()
-        blank = self.blanks.get((dtype, shape))
-        if blank is None:
-            if len(self.blanks) > 100:
-                self.blanks.clear()
-            blank = self.blanks[dtype, shape] = torch.empty(1, dtype=dtype, device=self.device).expand(shape)
-        return torch.empty_like(blank, memory_format=torch.contiguous_format)
+        self.native = _binding().cache(ctypes.addressof(self.struct), self.device.index)
 
     @classmethod
     def empty(cls, B: int, H: int, D: int, max_tokens: int, device="cuda", bounds: bool = True,
@@ -608,48 +616,17 @@ class Q8Cache:
 def _check_cache(cache, name="cache"):
     if type(cache) is not Q8Cache:
         raise TypeError(f"{name} must be a Q8Cache")
-    return cache.index
+    return cache.native
 
 
-def _refuse_other_device(t, name, index):
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
-
-
-def _whole(t, name, dtype, shape, index):
-    """The address of a contiguous tensor of this type and shape on device
-    `index`: one test on the common path, the specific error otherwise."""
-    try:
-        if t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    p = _check(t, name, dtype, shape)
-    _refuse_other_device(t, name, index)
-    return p
-
-
-def _view(t, name, dtype, shape, index):
-    """The same for a bf16 [B, H, T, D] view with unit stride along D."""
-    try:
-        if t.get_device() == index and t.dtype is dtype and t.shape == shape and t.stride(3) == 1:
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    p = _check_view(t, name, shape)
-    _refuse_other_device(t, name, index)
-    return p
-
-
-def _on_stream(stream, fn, cache, *args):
+def _on_stream(stream, cache, fn, *args):
     """fn(*args) on `stream`: what it allocates comes from that stream's memory,
     which no earlier work on the current stream still uses, and what it returns
     stays allocated while the current stream, for the caller, uses it."""
     cuda = _torch().cuda
-    index = _check_cache(cache)
-    if stream.device_index != index:
-        raise ValueError(f"stream must be on cuda:{index}, got cuda:{stream.device_index}")
-    current = cuda.current_stream(index)
+    if stream.device_index != cache.device.index:
+        raise ValueError(f"stream must be on {cache.device}, got cuda:{stream.device_index}")
+    current = cuda.current_stream(cache.device)
     with cuda.stream(stream):
         results = fn(*args)
     if stream != current and results is not None:
@@ -658,60 +635,24 @@ def _on_stream(stream, fn, cache, *args):
     return results
 
 
-def _call(fn, where, index, *args):
-    """The library call on device `index`, on its current stream."""
-    C = _torch()._C
-    if C._cuda_getDevice() == index:
-        status = fn(*args, C._cuda_getCurrentRawStream(index))
-    else:
-        with _torch().cuda.device(index):
-            status = fn(*args, C._cuda_getCurrentRawStream(index))
-    if status != 0:
-        raise AttnError(status, where)
-
-
 def attn_q8_append(cache, k, v, lens, new_lens=None, stream=None) -> None:
     """Takes the newest tokens' keys and values (bf16 [B, H, n, D], contiguous
     or strided views) into the cache.  ``lens`` [B] int32 counts them already;
     ``new_lens`` [B] int32: how many of the n rows are sequence b's (the first
     ones; None: all n)."""
+    native = _check_cache(cache)
     if stream is not None:
-        return _on_stream(stream, attn_q8_append, cache, cache, k, v, lens, new_lens)
-    index = _check_cache(cache)
-    bf16, i32, _ = cache.types
-    n = k.shape[2] if k.dim() == 4 else _shape4(k)
-    shape = (cache.B, cache.H, n, cache.D)
-    kp, vp = _view(k, "k", bf16, shape, index), _view(v, "v", bf16, shape, index)
-    lp = _whole(lens, "lens", i32, cache.batch, index)
-    np_ = None if new_lens is None else _whole(new_lens, "new_lens", i32, cache.batch, index)
-    st = None if k.is_contiguous() and v.is_contiguous() else _strides_of(k, v)
-    _call(_lib.attn_q8_append, "attn_q8_append", index, cache.ref, kp, vp, n, lp, np_, st)
+        return _on_stream(stream, cache, _q8.append, native, k, v, lens, new_lens)
+    return _q8.append(native, k, v, lens, new_lens)
 
 
 def attn_q8_read(cache, lens, n: int, starts=None, k=None, v=None, stream=None):
     """Positions starts[b] .. + n - 1 (None: from 0) as the cache holds them,
     in bf16 [B, H, n, D], zero past a sequence's end.  Returns (k, v)."""
+    native = _check_cache(cache)
     if stream is not None:
-        return _on_stream(stream, attn_q8_read, cache, cache, lens, n, starts, k, v)
-    index = _check_cache(cache)
-    bf16, i32, _ = cache.types
-    shape = (cache.B, cache.H, int(n), cache.D)
-    if n < 1:
-        raise AttnError(-2, "attn_q8_read")
-    lp = _whole(lens, "lens", i32, cache.batch, index)
-    sp = None if starts is None else _whole(starts, "starts", i32, cache.batch, index)
-    if k is None:
-        k = cache.new(bf16, shape)
-        kp = k.data_ptr()
-    else:
-        kp = _whole(k, "k", bf16, shape, index)
-    if v is None:
-        v = cache.new(bf16, shape)
-        vp = v.data_ptr()
-    else:
-        vp = _whole(v, "v", bf16, shape, index)
-    _call(_lib.attn_q8_read, "attn_q8_read", index, cache.ref, lp, sp, int(n), kp, vp)
-    return k, v
+        return _on_stream(stream, cache, _q8.read, native, lens, n, starts, k, v)
+    return _q8.read(native, lens, n, starts, k, v)
 
 
 _Q8_WEIGHT = {None: 0, "set": 1, "add": 2}
@@ -719,7 +660,7 @@ _Q8_WEIGHT = {None: 0, "set": 1, "add": 2}
 
 def attn_q8_decode_workspace_bytes(cache, H: int, Tq: int, blocks_n: int = 0, weight: Optional[str] = None) -> int:
     opts = attn_q8_decode_options(None, blocks_n, _Q8_WEIGHT[weight])
-    return int(_lib.attn_q8_decode_workspace_bytes(cache.ref, H, Tq, ctypes.byref(opts)))
+    return int(_lib.attn_q8_decode_workspace_bytes(ctypes.byref(cache.struct), H, Tq, ctypes.byref(opts)))
 
 
 def attn_q8_decode(q, cache, lens, o=None, lse=None, scale: Optional[float] = None, blocks=None,
@@ -730,78 +671,27 @@ def attn_q8_decode(q, cache, lens, o=None, lse=None, scale: Optional[float] = No
     blocks to attend to (the open one always is).  ``weight``: "set" or "add"
     to keep the attention weight of each closed block in cache.weight.
     Returns (O [B, Hq, Tq, D], lse [B, Hq, Tq])."""
-    if stream is not None:
-        return _on_stream(stream, attn_q8_decode, cache, q, cache, lens, o, lse, scale, blocks, weight, workspace)
-    index = _check_cache(cache)
-    bf16, i32, f32 = cache.types
-    _, H, Tq, D = q.shape if q.dim() == 4 else _shape4(q)
+    native = _check_cache(cache)
     keep = _Q8_WEIGHT.get(weight)
     if keep is None:
         raise ValueError("weight must be None, 'set' or 'add'")
-    shape = (cache.B, H, Tq, cache.D)
-    qp = _view(q, "q", bf16, shape, index)
-    lp = _whole(lens, "lens", i32, cache.batch, index)
-    plain = q.is_contiguous()
-    if o is None:
-        o = cache.new(bf16, shape)
-        op = o.data_ptr()
-    else:
-        op = _view(o, "o", bf16, shape, index)
-    if lse is None:
-        lse = cache.new(f32, shape[:3])
-        ep = lse.data_ptr()
-    else:
-        ep = _whole(lse, "lse", f32, shape[:3], index)
-    n, opts = 0, None
-    if blocks is not None:
-        if not isinstance(blocks, _torch().Tensor) or blocks.dim() != 4 or blocks.shape[3] < 1:
-            raise ValueError("blocks must be a [B, H, Tq, n] tensor")
-        n = blocks.shape[3]
-        opts = attn_q8_decode_options(_whole(blocks, "blocks", i32, (cache.B, cache.H, Tq, n), index), n, keep)
-    elif keep:
-        opts = attn_q8_decode_options(None, 0, keep)
-    if workspace is None:
-        need = cache.needs.get((H, Tq, n, keep))
-        if need is None:
-            need = int(_lib.attn_q8_decode_workspace_bytes(cache.ref, H, Tq, opts))
-            cache.needs[(H, Tq, n, keep)] = need
-        if need:
-            workspace = cache.k_codes.new_empty(need)
-    elif not workspace.is_contiguous() or workspace.get_device() != index:
-        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
-    wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = None if plain and o.is_contiguous() else _strides_of(q, o)
-    _call(_lib.attn_q8_decode, "attn_q8_decode", index, cache.ref, qp, op, ep, lp, H, Tq,
-          1.0 / math.sqrt(D) if scale is None else float(scale), st, opts, wp, wn)
-    return o, lse
+    if stream is not None:
+        return _on_stream(stream, cache, _q8.decode, native, q, lens, o, lse, scale, blocks, keep, workspace)
+    return _q8.decode(native, q, lens, o, lse, scale, blocks, keep, workspace)
 
 
 def attn_q8_select(q, cache, lens, n: int, blocks=None, stream=None):
     """The n closed blocks that each query of q (as in attn_q8_decode) is
     likely to attend to most, by a bound on their keys' products with it:
     int32 [B, H, Tq, n], ascending, -1 behind the last."""
+    native = _check_cache(cache)
     if stream is not None:
-        return _on_stream(stream, attn_q8_select, cache, q, cache, lens, n, blocks)
-    index = _check_cache(cache)
-    bf16, i32, _ = cache.types
-    _, H, Tq, _ = q.shape if q.dim() == 4 else _shape4(q)
-    if n < 1:
-        raise AttnError(-2, "attn_q8_select")
-    shape = (cache.B, cache.H, Tq, int(n))
-    qp = _view(q, "q", bf16, (cache.B, H, Tq, cache.D), index)
-    lp = _whole(lens, "lens", i32, cache.batch, index)
-    if blocks is None:
-        blocks = cache.new(i32, shape)
-        bp = blocks.data_ptr()
-    else:
-        bp = _whole(blocks, "blocks", i32, shape, index)
-    st = None if q.is_contiguous() else _strides_of(q)
-    _call(_lib.attn_q8_select, "attn_q8_select", index, cache.ref, qp, lp, bp, int(n), H, Tq, st)
-    return blocks
+        return _on_stream(stream, cache, _q8.select, native, q, lens, n, blocks)
+    return _q8.select(native, q, lens, n, blocks)
 
 
 def attn_q8_evict_workspace_bytes(cache) -> int:
-    return int(_lib.attn_q8_evict_workspace_bytes(cache.ref))
+    return int(_lib.attn_q8_evict_workspace_bytes(ctypes.byref(cache.struct)))
 
 
 def attn_q8_evict(cache, lens, keep: int, sink: int = 0, recent: int = 1, out=None, lens_out=None, kept=None,
@@ -811,34 +701,8 @@ def attn_q8_evict(cache, lens, keep: int, sink: int = 0, recent: int = 1, out=No
     moved to the front of ``out`` (None: of the cache itself).  Returns
     (lens_out [B], kept [B, H, keep]: the places the blocks came from, -1
     behind the last)."""
+    native = _check_cache(cache)
+    to = native if out is None else _check_cache(out, "out")
     if stream is not None:
-        return _on_stream(stream, attn_q8_evict, cache, cache, lens, keep, sink, recent, out, lens_out, kept, workspace)
-    index = _check_cache(cache)
-    i32 = cache.types[1]
-    out = cache if out is None else out
-    if _check_cache(out, "out") != index:
-        raise ValueError(f"out must be on cuda:{index}, got {out.device}")
-    if keep < 1:
-        raise AttnError(-2, "attn_q8_evict")
-    lp = _whole(lens, "lens", i32, cache.batch, index)
-    if lens_out is None:
-        lens_out = cache.new(i32, cache.batch)
-        op = lens_out.data_ptr()
-    else:
-        op = _whole(lens_out, "lens_out", i32, cache.batch, index)
-    shape = (cache.B, cache.H, int(keep))
-    if kept is None:
-        kept = cache.new(i32, shape)
-        kp = kept.data_ptr()
-    else:
-        kp = _whole(kept, "kept", i32, shape, index)
-    wp, wn = None, 0
-    if workspace is None and op == lp:  # the only case that needs one
-        workspace = cache.k_codes.new_empty(attn_q8_evict_workspace_bytes(cache))
-    if workspace is not None:
-        if not workspace.is_contiguous() or workspace.get_device() != index:
-            raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
-        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call(_lib.attn_q8_evict, "attn_q8_evict", index, cache.ref, out.ref, lp, op, kp, int(keep), int(sink),
-          int(recent), wp, wn)
-    return lens_out, kept
+        return _on_stream(stream, cache, _q8.evict, native, to, lens, keep, sink, recent, lens_out, kept, workspace)
+    return _q8.evict(native, to, lens, keep, sink, recent, lens_out, kept, workspace)

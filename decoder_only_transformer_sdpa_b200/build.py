@@ -4,14 +4,18 @@ repository).  Run ``python decoder_only_transformer_sdpa_b200/build.py``
 (a plain script: it does not import the package, which needs the library).
 ``--debug`` builds ``libattn_debug.so`` instead: the same kernels with the
 device-side bounds checks compiled in (-DATTN_DEVICE_CHECKS); select it with
-the ATTN_LIBRARY environment variable."""
+the ATTN_LIBRARY environment variable.  ``_q8.so``, the Python module of the
+8-bit cache's calls, is host code against torch's headers, built by g++ with
+either."""
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -22,6 +26,7 @@ LIB_DEBUG = os.path.join(HERE, "libattn_debug.so")
 ROOT = os.path.dirname(HERE)
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+CXX = "g++"
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
          f"-I{os.path.join(ROOT, 'include')}", "-Xptxas", "-warn-spills"]
@@ -34,6 +39,25 @@ def _sources():
 def _deps():
     return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.h"))) + \
         sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(ROOT, "include", "attn.h")]
+
+
+def build_binding(force: bool = False) -> str:
+    """The module _q8 (csrc/q8_binding.cpp); torch is found but not imported."""
+    src, so = os.path.join(CSRC, "q8_binding.cpp"), os.path.join(HERE, "_q8.so")
+    deps = [src, os.path.join(ROOT, "include", "attn.h")]
+    if not force and os.path.exists(so) and all(os.path.getmtime(p) <= os.path.getmtime(so) for p in deps):
+        return so
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+    tmp = so + f".tmp{os.getpid()}"
+    r = subprocess.run([CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", *(f"-I{d}" for d in include),
+                        src, "-o", tmp, "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+                        "-ltorch_python"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CXX} failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, so)
+    return so
 
 
 def up_to_date(lib: str = LIB) -> bool:
@@ -57,6 +81,7 @@ def _compile(src: str, verbose_ptxas: bool, debug: bool = False) -> str:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False) -> str:
+    build_binding(force)
     lib = LIB_DEBUG if debug else LIB
     if not force and up_to_date(lib):
         return lib

@@ -196,3 +196,56 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
                  lambda: A.attn_q8_evict(None, q, 1)):
         with pytest.raises(TypeError, match="Q8Cache"):
             call()
+
+
+class TestBinding:
+    """The module behind the binding, given a structure and CPU tensors: what it refuses before it touches a device."""
+
+    @staticmethod
+    def module():
+        m = A._binding()
+        return m, m.cache(ctypes.addressof(cache(B=1, H=2, D=64)), 0)
+
+    def test_tensors(self):
+        import torch
+        m, c = self.module()
+        q, lens = torch.zeros(1, 2, 1, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
+        for call in (lambda q: m.append(c, q, q, lens, None), lambda q: m.decode(c, q, lens, None, None, None, None, 0, None),
+                     lambda q: m.select(c, q, lens, 1, None)):
+            with pytest.raises(ValueError, match="must be a CUDA tensor"):
+                call(q)
+            with pytest.raises(ValueError, match="expected"):
+                call(q[0])
+            for bad in (None, 3, "q", [q]):
+                with pytest.raises(TypeError, match="torch.Tensor"):
+                    call(bad)
+        with pytest.raises(ValueError, match="lens must be a CUDA tensor"):
+            m.read(c, lens, 3, None, None, None)
+        with pytest.raises(ValueError, match="lens must be a CUDA tensor"):
+            m.evict(c, c, lens, 3, 0, 0, None, None, None)
+        with pytest.raises(TypeError, match="lens must be a torch.Tensor"):
+            m.read(c, None, 3, None, None, None)
+
+    def test_numbers(self):
+        m, c = self.module()
+        for n in (0, -1, 64 * 32769 + 1, 2**31, 2**70):
+            with pytest.raises(A.AttnError) as e:
+                m.read(c, None, n, None, None, None)
+            assert e.value.status == E_SHAPE
+        for keep, sink, recent in ((0, 0, 0), (32769, 0, 0), (2**40, 0, 0), (3, -1, 0), (3, 0, 2**33)):
+            with pytest.raises(A.AttnError) as e:
+                m.evict(c, c, None, keep, sink, recent, None, None, None)
+            assert e.value.status == E_SHAPE
+        with pytest.raises(TypeError):
+            m.read(c, None, 1.5, None, None, None)
+
+    def test_arguments(self):
+        m, c = self.module()
+        for f in (m.append, m.read, m.decode, m.select, m.evict):
+            with pytest.raises(TypeError, match="arguments"):
+                f(c)
+        with pytest.raises(ValueError):  # not a cache's capsule
+            m.read(object(), None, 1, None, None, None)
+        m2, c2 = m, m.cache(ctypes.addressof(cache(B=1, H=2, D=64)), 1)
+        with pytest.raises(ValueError, match="out must be on cuda:0"):
+            m2.evict(c, c2, None, 1, 0, 0, None, None, None)

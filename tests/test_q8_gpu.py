@@ -1,6 +1,8 @@
 """The 8-bit block cache on the GPU against its definition in 64 bits
 (tests/q8_reference.py): what an append holds bit by bit, the attention within
 bounds derived there, the choice of blocks and evictions exactly."""
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -939,6 +941,39 @@ def test_results_do_not_depend_on_the_run():
         first = first or now
         assert all(torch.equal(x, y) for x, y in zip(now, first))
     assert status() == 0
+
+
+def test_outputs_are_new_or_the_lent_ones_and_nothing_is_kept():
+    k, v = tokens(91, 1, 2, 200, 64)
+    c, L = filled(k, v, (200,))
+    q = queries(14, 1, 2, 1, 64).to(dev())
+    o, lse = torch.empty_like(q), torch.empty(1, 2, 1, device=dev())
+    kept, after = torch.empty(1, 2, 9, dtype=torch.int32, device=dev()), torch.empty(1, dtype=torch.int32, device=dev())
+    blocks, room = torch.empty(1, 2, 1, 2, dtype=torch.int32, device=dev()), torch.empty(1, 2, 200, 64, dtype=torch.bfloat16, device=dev())
+    lent = (q, L, o, lse, kept, after, blocks, room)
+
+    def calls():
+        got = A.attn_q8_decode(q, c, L, o=o, lse=lse)
+        assert got[0] is o and got[1] is lse
+        assert A.attn_q8_select(q, c, L, 2, blocks=blocks) is blocks
+        x, y = A.attn_q8_read(c, L, 200, k=room)
+        assert x is room and y is not room
+        got = A.attn_q8_evict(c, L, 9, lens_out=after, kept=kept)
+        assert got[0] is after and got[1] is kept
+        for bad in (lambda: A.attn_q8_decode(q, c, L, o=o, lse=o), lambda: A.attn_q8_decode(q, c, L, o=o, lse=lse, scale=-1.0),
+                    lambda: A.attn_q8_decode(q, c, L, workspace=L.cpu()), lambda: A.attn_q8_read(c, L, 200, k=room, v=o),
+                    lambda: A.attn_q8_decode(q, c, L, scale="1"), lambda: A.attn_q8_evict(c, L, 9, kept=after)):
+            with pytest.raises((TypeError, ValueError, A.AttnError)):
+                bad()
+
+    calls()
+    torch.cuda.synchronize()
+    counts, held = [sys.getrefcount(t) for t in lent], torch.cuda.memory_allocated()
+    for _ in range(20):
+        calls()
+    assert [sys.getrefcount(t) for t in lent] == counts
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() == held and status() == 0
 
 
 def test_binding_refusals_on_the_gpu():
