@@ -37,6 +37,8 @@ constexpr int kMaxCluster = 8;
 constexpr int kBits = 10;  // of a pass: two bins a thread
 static_assert(1 << kBits == 2 * kThreads, "two bins a thread");
 
+constexpr int kRanked = 256;  // up to so many keys are ranked by comparing each with each
+
 struct SelectSmem {
     alignas(8) uint32_t hist[1 << kBits];
     uint32_t low[kWarps], high[kWarps], sum[kWarps], ties[kWarps];
@@ -70,6 +72,29 @@ __device__ void largest(const uint32_t *key, int count, int n, int32_t *list, Se
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (count <= n) {
         for (int i = tid; i < n; i += kThreads) list[i] = i < count ? i : -1;
+        return;
+    }
+    if (count <= kRanked) {
+        // ---- few keys: each one's rank, its comparisons shared by the threads of one index
+        const int width = count <= kRanked / 2 ? kRanked / 2 : kRanked, parts = kThreads / width;
+        const int i = tid % width, per = (count + parts - 1) / parts, j0 = tid / width * per, j1 = min(count, j0 + per);
+        const uint32_t mine = i < count ? key[i] : 0u;
+        uint32_t rank = 0;
+#pragma unroll 8
+        for (int j = j0; j < j1; ++j) {
+            const uint32_t x = key[j];
+            rank += x > mine || (x == mine && j < i);
+        }
+        sm.hist[tid] = rank;
+        __syncthreads();
+        for (int y = 1; y < parts; ++y) rank += sm.hist[(tid + y * width) % kThreads];
+        const bool in = tid < count && rank < (uint32_t)n;
+        const uint32_t together = __ballot_sync(0xffffffffu, in);
+        if (lane == 0) sm.sum[warp] = __popc(together);
+        __syncthreads();
+        uint32_t out = __popc(together & ((1u << lane) - 1u));
+        for (int y = 0; y < warp; ++y) out += sm.sum[y];
+        if (in) list[out] = tid;
         return;
     }
     // ---- the bits in which keys differ
