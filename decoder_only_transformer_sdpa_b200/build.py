@@ -52,7 +52,7 @@ def build_binding(force: bool = False) -> str:
                sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
     tmp = so + f".tmp{os.getpid()}"
     r = subprocess.run([CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", *(f"-I{d}" for d in include),
-                        src, "-o", tmp, "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+                        src, "-o", tmp, "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
                         "-ltorch_python"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{CXX} failed on {src}:\n{r.stdout}\n{r.stderr}")

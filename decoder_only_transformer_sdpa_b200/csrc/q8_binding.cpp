@@ -3,7 +3,7 @@
 // Checks what a call gets, makes the outputs that it was not lent and hands
 // addresses, strides and the device's current stream to the entry points of
 // libattn.so.  What bounds it is the host's time: a decode of one token is 4.5 us
-// of GPU time, and issuing it takes 5.4 us from here, 2.4 us of that the launch;
+// of GPU time, and issuing it takes 5.0 us from here, 2.4 us of that the launch;
 // the same steps from Python (each tensor's attributes one by one, then ctypes)
 // took 11.6 us, and the GPU waited for them.
 //
@@ -13,7 +13,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/DynamicTypes.h>
@@ -107,6 +107,11 @@ T *whole(PyObject *o, const char *name, at::ScalarType type, at::IntArrayRef sha
     return static_cast<T *>(t.data_ptr());
 }
 
+// A new contiguous tensor, straight from the allocator: every element of it is written by the call.
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int index) {
+    return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, (c10::DeviceIndex)index), std::nullopt);
+}
+
 // The same, made where it is not lent; `kept` holds a reference to it.
 template <typename T>
 T *output(PyObject *o, const char *name, at::ScalarType type, at::IntArrayRef shape, int index, THPObjectPtr &kept) {
@@ -116,7 +121,7 @@ T *output(PyObject *o, const char *name, at::ScalarType type, at::IntArrayRef sh
         kept = o;
         return p;
     }
-    at::Tensor t = at::empty(shape, at::TensorOptions(type).device(at::kCUDA, (c10::DeviceIndex)index));
+    at::Tensor t = fresh(shape, type, index);
     T *p = static_cast<T *>(t.data_ptr());
     kept = THPVariable_Wrap(std::move(t));
     if (!kept) throw python_error();
@@ -160,7 +165,7 @@ struct Workspace {
     }
     void make(size_t n, int index) {
         if (n == 0) return;
-        own = at::empty({(int64_t)n}, at::TensorOptions(at::kByte).device(at::kCUDA, (c10::DeviceIndex)index));
+        own = fresh((int64_t)n, at::kByte, index);
         at = own.data_ptr();
         bytes = n;
     }
