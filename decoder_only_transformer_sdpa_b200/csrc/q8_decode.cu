@@ -134,7 +134,9 @@ struct Smem {
     uint64_t full[kWarps][kSlots];
     float m[kWarps][kRows], l[kWarps][kRows];
     float mc[kRows], lc[kRows];  // the CTA's maximum and sum
+    float by[kRows];             // what the CTA's outputs are multiplied by
     float total[kRows];          // log2 of each row's sum (for the blocks' weights)
+    long long to[kRows];         // where each row's output goes, in elements of o
     int abort;
 };
 
@@ -149,6 +151,7 @@ struct DecodeArgs {
     const int32_t *list;  // NULL: every block
     int list_n;
     int H, G, Tq;   // query heads, heads of a group, new tokens
+    unsigned per_tq;  // 2^16 / Tq rounded up: (r * per_tq) >> 16 is r / Tq for r * Tq < 2^16, and r < 64 * 16
     int rows;       // rows of a group: G * Tq, or G with lists (a group is then one token)
     int tiles;      // row tiles of a group
     int tile_rows;  // rows of a tile
@@ -257,9 +260,11 @@ __device__ __forceinline__ void runs_of_tile(const DecodeArgs &a, unsigned group
 }
 
 // Head in the group and token of row `row` of a group.
-__device__ __forceinline__ int row_head(const DecodeArgs &a, int row) { return a.list ? row : row / a.Tq; }
+__device__ __forceinline__ int row_head(const DecodeArgs &a, int row) {
+    return a.list ? row : (int)((unsigned)row * a.per_tq >> 16);
+}
 __device__ __forceinline__ int row_token(const DecodeArgs &a, const Where &w, int row) {
-    return a.list ? w.r0 : row % a.Tq;
+    return a.list ? w.r0 : row - row_head(a, row) * a.Tq;
 }
 
 // Running softmax state of a warp: this lane's rows 2t and 2t + 1 of each row
@@ -444,9 +449,8 @@ __device__ __forceinline__ void open_tokens(State<D, NT> &st, float qscale, cons
     }
 }
 
-// One result (maximum folded into f, sum l1, output o1) into a joint one.
-__device__ __forceinline__ void join(float4 &o, float &l, float f, float l1, const float4 &o1) {
-    l = fmaf(f, l1, l);
+// f times one output into a joint one.
+__device__ __forceinline__ void add(float4 &o, float f, const float4 &o1) {
     o.x = fmaf(f, o1.x, o.x);
     o.y = fmaf(f, o1.y, o.y);
     o.z = fmaf(f, o1.z, o.z);
@@ -456,18 +460,20 @@ __device__ __forceinline__ void join(float4 &o, float &l, float f, float l1, con
 // log2 of a row's sum, in the units of the blocks' sums; a row that sees nothing gives nothing.
 __device__ __forceinline__ float row_total(float m, float l) { return l == 0.f ? INFINITY : m + lg2(l); }
 
-// Four channels of row `r` of a group, and with the first ones its lse.
-__device__ __forceinline__ void write_row(const DecodeArgs &a, const Where &w, int r, int ch, float m, float l,
-                                          const float4 &o) {
-    const int head = w.h * a.G + row_head(a, r), tok = row_token(a, w, r);
-    const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: zeros
-    *reinterpret_cast<uint2 *>(a.o + (long long)w.b * a.so.b + (long long)head * a.so.h + (long long)tok * a.so.t +
-                               ch) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (ch == 0) {
-        a.lse[((long long)w.b * a.H + head) * a.Tq + tok] = l == 0.f ? -INFINITY : (m + (log2f(l) - kPShift)) * kLn2;
-        if (a.part.total) a.part.total[w.bh * (a.tiles * a.tile_rows) + r] = row_total(m, l);
-    }
+// Row `r` of a group: where its output goes, and its lse.
+__device__ __forceinline__ long long row_place(const DecodeArgs &a, const Where &w, int r) {
+    return (long long)w.b * a.so.b + (long long)(w.h * a.G + row_head(a, r)) * a.so.h +
+           (long long)row_token(a, w, r) * a.so.t;
+}
+__device__ __forceinline__ void write_lse(const DecodeArgs &a, const Where &w, int r, float m, float l) {
+    a.lse[((long long)w.b * a.H + w.h * a.G + row_head(a, r)) * a.Tq + row_token(a, w, r)] =
+        l == 0.f ? -INFINITY : (m + (log2f(l) - kPShift)) * kLn2;
+    if (a.part.total) a.part.total[w.bh * (a.tiles * a.tile_rows) + r] = row_total(m, l);
+}
+// What a row's sums are multiplied by; nothing seen: zeros.
+__device__ __forceinline__ float row_factor(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ void write_four(__nv_bfloat16 *to, const float4 &o, float by) {
+    *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16x2(o.x * by, o.y * by), pack_bf16x2(o.z * by, o.w * by));
 }
 
 // weight[j] (+)= sum over the rows of exp(block j's log-sum - the row's log-sum),
@@ -867,29 +873,44 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
         }
         __syncthreads();
         const int here = min(kRows, a.rows - w.tile * kRows);
-        for (int e = tid; e < here * (D / 4); e += kThreads) {
-            const int row = e / (D / 4), ch = 4 * (e % (D / 4));
-            float m = -INFINITY, l = 0.f;
+        if (tid < here) {
+            // a thread a row: its maximum and sum, the warps' factors (in their maxima's place), where it goes
+            float m = -INFINITY, l = 0.f, f[kWarps];
 #pragma unroll
-            for (int y = 0; y < kWarps; ++y) m = fmaxf(m, sm.m[y][row]);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int y = 0; y < kWarps; ++y) m = fmaxf(m, sm.m[y][tid]);
             const float safe = m == -INFINITY ? 0.f : m;
 #pragma unroll
-            for (int y = 0; y < kWarps; ++y)
-                join(o, l, ex2(sm.m[y][row] - safe), sm.l[y][row], *reinterpret_cast<const float4 *>(&sm.part[y][row][ch]));
-            if (a.cluster == 1) {
-                write_row(a, w, w.tile * kRows + row, ch, m, l, o);
-            } else if (a.cluster) {
-                *reinterpret_cast<float4 *>(&sm.o[row][ch]) = o;
+            for (int y = 0; y < kWarps; ++y) {
+                f[y] = ex2(sm.m[y][tid] - safe);
+                l = fmaf(f[y], sm.l[y][tid], l);
+            }
+            const float by = a.cluster == 1 ? row_factor(l) : 1.f;
+#pragma unroll
+            for (int y = 0; y < kWarps; ++y) sm.m[y][tid] = f[y];
+            sm.by[tid] = by;
+            const int r = w.tile * kRows + tid;
+            if (a.cluster) {
+                sm.mc[tid] = m;
+                sm.lc[tid] = l;
+                sm.to[tid] = row_place(a, w, r);
+                if (a.cluster == 1) write_lse(a, w, r, m, l);
             } else {
-                const long long to = ((long long)blockIdx.x + group) * kRows + row;
-                *reinterpret_cast<float4 *>(a.part.o + to * D + ch) = o;
-                if (ch == 0) a.part.ml[to] = make_float2(m, l);
+                a.part.ml[((long long)blockIdx.x + group) * kRows + tid] = make_float2(m, l);
             }
-            if (a.cluster && ch == 0) {
-                sm.mc[row] = m;
-                sm.lc[row] = l;
-            }
+        }
+        __syncthreads();
+#pragma unroll 2
+        for (int e = tid; e < here * (D / 4); e += kThreads) {
+            const int row = e / (D / 4), ch = 4 * (e % (D / 4));
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int y = 0; y < kWarps; ++y) add(o, sm.m[y][row], *reinterpret_cast<const float4 *>(&sm.part[y][row][ch]));
+            if (a.cluster == 1)
+                write_four(a.o + sm.to[row] + ch, o, sm.by[row]);
+            else if (a.cluster)
+                *reinterpret_cast<float4 *>(&sm.o[row][ch]) = o;
+            else
+                *reinterpret_cast<float4 *>(a.part.o + (((long long)blockIdx.x + group) * kRows + row) * D + ch) = o;
         }
         if (!a.cluster) {
             // ---- the next row tile with units
@@ -920,10 +941,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
                 const float safe = m == -INFINITY ? 0.f : m;
 #pragma unroll
                 for (int y = 0; y < kMaxCluster; ++y)
-                    if (y < a.cluster)
-                        join(o, l, ex2(ms[y] - safe), *cluster.map_shared_rank(&sm.lc[row], y),
-                             *reinterpret_cast<const float4 *>(cluster.map_shared_rank(&sm.o[row][ch], y)));
-                write_row(a, w, w.tile * kRows + row, ch, m, l, o);
+                    if (y < a.cluster) {
+                        const float f = ex2(ms[y] - safe);
+                        l = fmaf(f, *cluster.map_shared_rank(&sm.lc[row], y), l);
+                        add(o, f, *reinterpret_cast<const float4 *>(cluster.map_shared_rank(&sm.o[row][ch], y)));
+                    }
+                write_four(a.o + sm.to[row] + ch, o, row_factor(l));
+                if (ch == 0) write_lse(a, w, w.tile * kRows + row, m, l);
             }
         }
         if (a.weigh) {
@@ -990,15 +1014,22 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 #pragma unroll 4
     for (int y = first + tid / kLanes; y <= last; y += kParts) {
         const float2 x = ml[(long long)y * kRows];
-        join(o, l, ex2(x.x - safe), x.y, *reinterpret_cast<const float4 *>(po + (long long)y * kRows * D));
+        const float f = ex2(x.x - safe);
+        l = fmaf(f, x.y, l);
+        add(o, f, *reinterpret_cast<const float4 *>(po + (long long)y * kRows * D));
     }
     so[tid / kLanes][tid % kLanes] = o;
     if (tid % kLanes == 0) sl[tid / kLanes] = l;
     __syncthreads();
     if (tid < kLanes) {
 #pragma unroll
-        for (int y = 1; y < kParts; ++y) join(o, l, 1.f, sl[y], so[y][tid]);
-        write_row(a, w, w.tile * kRows + row, 4 * tid, m, l, o);
+        for (int y = 1; y < kParts; ++y) {
+            l += sl[y];
+            add(o, 1.f, so[y][tid]);
+        }
+        const int r = w.tile * kRows + row;
+        write_four(a.o + row_place(a, w, r) + 4 * tid, o, row_factor(l));
+        if (tid == 0) write_lse(a, w, r, m, l);
     }
 }
 
@@ -1166,6 +1197,7 @@ cudaError_t q8_decode(const Q8Cache &c, const Q8Decode &d, int *err, cudaStream_
     a.H = d.H;
     a.G = d.H / c.H;
     a.Tq = d.Tq;
+    a.per_tq = (65536u + d.Tq - 1) / d.Tq;
     a.rows = p.rows;
     a.tiles = p.tiles;
     a.tile_rows = 8 * p.nt;
