@@ -100,7 +100,8 @@ struct Cfg {
     static constexpr int kCtas = NT == 1 || (NT == 2 && D < 128) ? 3 : 2;
     static constexpr int kHalves = D == 128 ? 2 : 1;  // slots of a block
     static constexpr int kSlots = D == 32 ? 4 : (kCtas == 3 ? 2 : 3);
-    static constexpr bool kQueriesInSmem = NT > 1;  // else in registers
+    static constexpr bool kQueriesInSmem = NT > 1;  // a warp prepares a row tile; else each the only one, in registers
+    static_assert(NT <= kWarps, "a warp a row tile");
     // tiles of 16 tokens (keys) or 16 channels (values) whose sums a warp forms side by side
     static constexpr int kAtOnce = NT == 4 ? 1 : D == 32 ? 2 : 4 / NT;
 };
@@ -131,6 +132,8 @@ struct Smem {
         };
     };
     uint2 q[Cfg<D, NT>::kQueriesInSmem ? NT : 1][Cfg<D, NT>::kQueriesInSmem ? D / 16 : 1][32];  // fragments
+    float down[kRows];  // their rows' factors
+    int seen[kRows];    // and the last position each sees
     uint64_t full[kWarps][kSlots];
     float m[kWarps][kRows], l[kWarps][kRows];
     float mc[kRows], lc[kRows];  // the CTA's maximum and sum
@@ -266,6 +269,10 @@ __device__ __forceinline__ int row_head(const DecodeArgs &a, int row) {
 __device__ __forceinline__ int row_token(const DecodeArgs &a, const Where &w, int row) {
     return a.list ? w.r0 : row - row_head(a, row) * a.Tq;
 }
+__device__ __forceinline__ const __nv_bfloat16 *query_row(const DecodeArgs &a, const Where &w, int row) {
+    return a.q + (long long)w.b * a.sq.b + (long long)(w.h * a.G + row_head(a, row)) * a.sq.h +
+           (long long)row_token(a, w, row) * a.sq.t;
+}
 
 // Running softmax state of a warp: this lane's rows 2t and 2t + 1 of each row
 // tile (t = lane % 4), and O^T with channels 16 i + g, + 8 (g = lane / 4).
@@ -374,10 +381,9 @@ __device__ __forceinline__ uint32_t clean_pair(uint32_t w, bool first, bool seco
 
 // 16 tokens of the open block, positions p0 .. p0 + 15 of a sequence of length
 // L: keys k and values v [16][D] in shared memory.
-template <int D, int NT>
-__device__ __forceinline__ void open_tokens(State<D, NT> &st, float qscale, const __nv_bfloat16 *(&qrow)[NT],
-                                            const int (&sees)[NT][2], const __nv_bfloat16 *k, const __nv_bfloat16 *v,
-                                            int p0, int L, int lane) {
+template <int D, int NT, typename Queries, typename Sees>
+__device__ __forceinline__ void open_tokens(State<D, NT> &st, float qscale, Queries queries, Sees sees,
+                                            const __nv_bfloat16 *k, const __nv_bfloat16 *v, int p0, int L, int lane) {
     const int g = lane >> 2, t = lane & 3;
     float s[1][NT][4], f[NT][2], sum[NT][2];
     {
@@ -389,7 +395,8 @@ __device__ __forceinline__ void open_tokens(State<D, NT> &st, float qscale, cons
             uint32_t q[D / 8];
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) q[i] = 0;
-            if (qrow[nt]) load_row<D>(q, qrow[nt], t);
+            const __nv_bfloat16 *row = queries(nt);
+            if (row) load_row<D>(q, row, t);
             s[0][nt][0] = s[0][nt][1] = s[0][nt][2] = s[0][nt][3] = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
@@ -398,7 +405,7 @@ __device__ __forceinline__ void open_tokens(State<D, NT> &st, float qscale, cons
             }
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                if (p0 + g + (x & 2) * 4 > sees[nt][x & 1]) s[0][nt][x] = -INFINITY;
+                if (p0 + g + (x & 2) * 4 > sees(nt, x & 1)) s[0][nt][x] = -INFINITY;
             f[nt][0] = f[nt][1] = qscale;
         }
     }
@@ -442,7 +449,7 @@ __device__ __forceinline__ void open_tokens(State<D, NT> &st, float qscale, cons
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         const float e = __bfloat162float(v[y * D + 16 * i + g + (x & 2) * 4]);
-                        if (!isfinite(e) && p0 + y <= sees[nt][x & 1])
+                        if (!isfinite(e) && p0 + y <= sees(nt, x & 1))
                             st.o[i][nt][x] = fmaf((x & 1) ? pb : pa, e, st.o[i][nt][x]);
                     }
             }
@@ -500,6 +507,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
     using Sm = Smem<D, NT>;
     constexpr int SL = Sm::kSlots, kRows = Sm::kRows, S = slab(D), kHalves = Cfg<D, NT>::kHalves,
                   kAtOnce = Cfg<D, NT>::kAtOnce;
+    constexpr bool kShared = Cfg<D, NT>::kQueriesInSmem;
     constexpr int kSide = kBlock * D;  // bytes of a block's keys, and of its values
     static_assert(sizeof(float) * kWarps * kRows * Sm::kPitch + sizeof(float) * kRows * D <= sizeof(Sm::ring),
                   "the outputs take no more than the rings");
@@ -533,21 +541,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
     bool ok = true;
     while (true) {
         const Where w = where(a, group);
-        // ---- queries: this lane's row g of each row tile (on their way while the lengths are)
-        uint32_t qx[NT][D / 8];
-        const __nv_bfloat16 *qrow[NT];
+        // ---- queries: this lane's row g of the warp's row tile (on their way while the lengths are)
+        uint32_t qx[D / 8];
+        const int my_tile = kShared ? warp : 0, my_row = w.tile * kRows + my_tile * 8 + g;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int row = w.tile * kRows + nt * 8 + g;
-            qrow[nt] = nullptr;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) qx[nt][i] = 0;
-            if (row < a.rows) {
-                qrow[nt] = a.q + (long long)w.b * a.sq.b + (long long)(w.h * a.G + row_head(a, row)) * a.sq.h +
-                           (long long)row_token(a, w, row) * a.sq.t;
-                load_row<D, true>(qx[nt], qrow[nt], t);
-            }
-        }
+        for (int i = 0; i < D / 8; ++i) qx[i] = 0;
+        const __nv_bfloat16 *my_q = my_tile < NT && my_row < a.rows ? query_row(a, w, my_row) : nullptr;
+        if (my_q) load_row<D, true>(qx, my_q, t);
+        auto queries = [&](int nt) -> const __nv_bfloat16 * {  // this lane's row of row tile nt
+            if constexpr (!kShared) return my_q;
+            const int row = w.tile * kRows + 8 * nt + g;
+            return row < a.rows ? query_row(a, w, row) : nullptr;
+        };
         int L = checked_length(a.lens[w.b], a.c.blocks, a.err);
         if (L < 0) L = 0;
         // ---- this warp's blocks: places first, first + step, ... below `count` (of all closed blocks, or of the list),
@@ -641,15 +646,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
         float2 sc = id >= 0 ? scales[id] : make_float2(0.f, 0.f);
 
         // ---- the queries as f16 fragments, and the factors of rows 2t, 2t + 1
-        uint32_t qf[Cfg<D, NT>::kQueriesInSmem ? 1 : NT][D / 8];
-        float rowf[NT][2];
-        int sees[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            uint32_t(&x)[D / 8] = qx[nt];
+        float rowf[2];
+        if (my_tile < NT) {
             uint32_t mx = 0;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) mx = __vmaxu2(mx, x[i] & 0x7fff7fffu);
+            for (int i = 0; i < D / 8; ++i) mx = __vmaxu2(mx, qx[i] & 0x7fff7fffu);
             mx = max(mx & 0xffffu, mx >> 16);
             mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -660,28 +661,46 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
             const float down = __uint_as_float((uint32_t)(127 - e) << 23) * a.qscale;
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
-                const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x[i]));
-                x[i] = pack_f16x2(f.x * up, f.y * up);
-                if constexpr (!Cfg<D, NT>::kQueriesInSmem) qf[nt][i] = x[i];
+                const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&qx[i]));
+                qx[i] = pack_f16x2(f.x * up, f.y * up);
             }
-            if constexpr (Cfg<D, NT>::kQueriesInSmem) {
+            if constexpr (kShared) {
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    if (warp == i % kWarps) sm.q[nt][i][lane] = make_uint2(x[2 * i], x[2 * i + 1]);
-            }
+                for (int i = 0; i < D / 16; ++i) sm.q[my_tile][i][lane] = make_uint2(qx[2 * i], qx[2 * i + 1]);
+                if (t == 0) sm.down[8 * my_tile + g] = down;
+            } else {
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                rowf[nt][y] = __shfl_sync(0xffffffffu, down, 4 * (2 * t + y));
-                const int r = w.tile * kRows + nt * 8 + 2 * t + y;
-                sees[nt][y] = r < a.rows ? L - a.Tq + row_token(a, w, r) : -1;
+                for (int y = 0; y < 2; ++y) rowf[y] = __shfl_sync(0xffffffffu, down, 4 * (2 * t + y));
             }
         }
-        if constexpr (Cfg<D, NT>::kQueriesInSmem) __syncthreads();
+        // the last position that row r of the tile sees
+        auto last_seen = [&](int r) { return r < a.rows - w.tile * kRows ? L - a.Tq + row_token(a, w, w.tile * kRows + r) : -1; };
+        int seen[2];
+        if constexpr (kShared) {
+            if (tid < kRows) sm.seen[tid] = last_seen(tid);
+            __syncthreads();
+        } else {
+            seen[0] = last_seen(2 * t);
+            seen[1] = last_seen(2 * t + 1);
+        }
+        // of rows 2t, 2t + 1 of a row tile: that, and their factors
+        auto sees = [&](int nt, int y) {
+            if constexpr (kShared)
+                return sm.seen[8 * nt + 2 * t + y];
+            else
+                return seen[y];
+        };
+        auto factor = [&](int nt, int y) {
+            if constexpr (kShared)
+                return sm.down[8 * nt + 2 * t + y];
+            else
+                return rowf[y];
+        };
         auto query = [&](int nt, int i) -> uint2 {
-            if constexpr (Cfg<D, NT>::kQueriesInSmem)
+            if constexpr (kShared)
                 return sm.q[nt][i][lane];
             else
-                return make_uint2(qf[nt][2 * i], qf[nt][2 * i + 1]);
+                return make_uint2(qx[2 * i], qx[2 * i + 1]);
         };
 
         State<D, NT> st;
@@ -696,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
         // ---- the open block
         if (tokens && (ok = wait())) {
             const __nv_bfloat16 *k = reinterpret_cast<const __nv_bfloat16 *>(sm.ring[warp][slot]);
-            open_tokens<D, NT>(st, a.qscale, qrow, sees, k, k + 16 * D, closed * kBlock + open_at, L, lane);
+            open_tokens<D, NT>(st, a.qscale, queries, sees, k, k + 16 * D, closed * kBlock + open_at, L, lane);
             next();
         }
 
@@ -765,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
                     for (int u = 0; u < 4; ++u)
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
-                            if (p0 + 16 * (g >> 1) + 4 * u + (g & 1) + (x & 2) > sees[nt][x & 1])
+                            if (p0 + 16 * (g >> 1) + 4 * u + (g & 1) + (x & 2) > sees(nt, x & 1))
                                 sv[u][nt][x] = -INFINITY;
             }
             float f[NT][2], sum[NT][2];
@@ -773,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(con
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    f[nt][x] = sc.x * rowf[nt][x];
+                    f[nt][x] = sc.x * factor(nt, x);
                     // a block of zeros: any factor gives its scores 0 and keeps -inf what it is (a NaN stays)
                     if (f[nt][x] == 0.f) f[nt][x] = 1.f;
                 }
