@@ -29,9 +29,9 @@
 //   * little work: the CTAs of a cluster share a row tile, each block going to
 //     the next of their warps, and they join their results through distributed
 //     shared memory: one launch;
-//   * much of it: CTAs that fill the GPU twice take equal runs of all blocks of
-//     all row tiles, whatever the sequences' lengths (which only the kernel
-//     knows); a second kernel joins what the runs left of each row tile.
+//   * much of it: as many CTAs as the GPU holds, or twice as many, take equal runs
+//     of all blocks of all row tiles, whatever the sequences' lengths (which only
+//     the kernel knows); a second kernel joins what the runs left of each row tile.
 //
 // The open block comes first, in bf16 from the ring of recent positions, 16
 // tokens a warp, with exact products and P as the sum of two bf16 numbers.
@@ -91,13 +91,16 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 // Warps of a CTA, slots of a warp's ring (a block, or half of one at D = 128),
 // and CTAs that an SM holds: three of 168 registers a thread, or two of 255 where
-// the sums take more (16 rows of 64 channels with three CTAs, spilling 36 bytes,
-// against two: 21.9 and 34.2 us on 432 row tiles, 14.4 and 13.7 on 6).
+// the sums take more (us with three / two CTAs; 16 rows of 64 channels, which
+// spill 108 bytes with three: 432 row tiles 23.5 / 57, 273 short ones 8.2 / 8.0,
+// 6 long ones 13.1 / 11.8; one row of 128 channels, which spills 136 bytes with
+// three: 128 long row tiles 64.6 / 59.4, 256 of 2048 tokens 23.9 / 22.0, 144 of
+// 500 tokens 9.7 / 9.1).
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 template <int D, int NT>
 struct Cfg {
-    static constexpr int kCtas = NT == 1 || (NT == 2 && D < 128) ? 3 : 2;
+    static constexpr int kCtas = D < 128 && NT <= 2 ? 3 : 2;
     static constexpr int kHalves = D == 128 ? 2 : 1;  // slots of a block
     static constexpr int kSlots = D == 32 ? 4 : (kCtas == 3 ? 2 : 3);
     static constexpr bool kQueriesInSmem = NT > 1;  // a warp prepares a row tile; else each the only one, in registers
