@@ -253,19 +253,38 @@ __global__ void __launch_bounds__(kReadThreads)
     if (block < L / kBlock) {
         const long long at = bh * c.blocks + block;
         const uint8_t *kc = c.k_codes + at * (kBlock * D), *vc = c.v_codes + at * (kBlock * D);
-        const float ks = c.scales[2 * at], vs = c.scales[2 * at + 1];
-        for (int e = tid; e < D * (kBlock / 16); e += kReadThreads) {
-            const int ch = e / (kBlock / 16), q = 4 * (e % (kBlock / 16));
-            const uint4 w = *reinterpret_cast<const uint4 *>(vc + ch * kBlock + 4 * q);
-            sv[ch][q] = w.x;
-            sv[ch][q + 1] = w.y;
-            sv[ch][q + 2] = w.z;
-            sv[ch][q + 3] = w.w;
+        // all loads first: a CTA's time is their latency
+        constexpr int kKeys = kBlock * kChunks / kReadThreads, kValues = (D * (kBlock / 16) + kReadThreads - 1) / kReadThreads;
+        auto wanted = [&](int t) { return p0 + t >= first && p0 + t < last; };
+        const float2 scale = reinterpret_cast<const float2 *>(c.scales)[at];
+        uint4 vw[kValues];
+#pragma unroll
+        for (int i = 0; i < kValues; ++i) {  // 16 tokens of a channel
+            const int e = tid + i * kReadThreads;
+            if (e < D * (kBlock / 16)) vw[i] = *reinterpret_cast<const uint4 *>(vc + 16 * e);
         }
-        for (int e = tid; e < kBlock * kChunks; e += kReadThreads) {
-            const int t = e / kChunks, ch = 8 * (e % kChunks);
-            if (p0 + t < first || p0 + t >= last) continue;
-            const uint2 w = *reinterpret_cast<const uint2 *>(kc + key_offset<D>(t, ch));
+        uint2 kw[kKeys];
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {  // eight channels of a token
+            const int e = tid + i * kReadThreads, t = e / kChunks, ch = 8 * (e % kChunks);
+            if (wanted(t)) kw[i] = *reinterpret_cast<const uint2 *>(kc + key_offset<D>(t, ch));
+        }
+        const float ks = scale.x, vs = scale.y;
+#pragma unroll
+        for (int i = 0; i < kValues; ++i) {
+            const int e = tid + i * kReadThreads, ch = e / (kBlock / 16), q = 4 * (e % (kBlock / 16));
+            if (e < D * (kBlock / 16)) {
+                sv[ch][q] = vw[i].x;
+                sv[ch][q + 1] = vw[i].y;
+                sv[ch][q + 2] = vw[i].z;
+                sv[ch][q + 3] = vw[i].w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+            const int e = tid + i * kReadThreads, t = e / kChunks, ch = 8 * (e % kChunks);
+            if (!wanted(t)) continue;
+            const uint2 w = kw[i];
             uint4 r;
             r.x = pack_bf16x2((int)((w.x & 255) - 128) * ks, (int)(((w.x >> 8) & 255) - 128) * ks);
             r.y = pack_bf16x2((int)(((w.x >> 16) & 255) - 128) * ks, (int)((w.x >> 24) - 128) * ks);
