@@ -91,16 +91,21 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 // Warps of a CTA, slots of a warp's ring (a block, or half of one at D = 128),
 // and CTAs that an SM holds: three of 168 registers a thread, or two of 255 where
-// the sums take more (us with three / two CTAs; 16 rows of 64 channels, which
-// spill 108 bytes with three: 432 row tiles 23.5 / 57, 273 short ones 8.2 / 8.0,
-// 6 long ones 13.1 / 11.8; one row of 128 channels, which spills 136 bytes with
-// three: 128 long row tiles 64.6 / 59.4, 256 of 2048 tokens 23.9 / 22.0, 144 of
-// 500 tokens 9.7 / 9.1).
+// the sums take more.  In between (32 rows of 32 channels, 16 of 64, 8 of 128),
+// where three CTAs spill 40 to 140 bytes a thread, three only where two would
+// leave row tiles waiting.  Us with three / two: 16 rows of 64, 432 row tiles 23.5
+// / 57, 273 short ones 8.2 / 8.0, 6 long ones 13.1 / 11.8; 32 rows of 32, 400 row
+// tiles 16.5 / 25.1; 8 rows of 128, 400 row tiles of 100 tokens 7.5 / 11.0 and of
+// 2000 tokens 41.4 / 40.6, 128 of up to 16384 tokens 64.6 / 59.4.
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-template <int D, int NT>
+constexpr int ctas_on_sm(int D, int nt, bool crowded) {
+    const int sums = D * nt;  // (of a thread, D / 4 each)
+    return sums <= 64 ? 3 : sums <= 128 && crowded ? 3 : 2;
+}
+template <int D, int NT, int Ctas>
 struct Cfg {
-    static constexpr int kCtas = D < 128 && NT <= 2 ? 3 : 2;
+    static constexpr int kCtas = Ctas;
     static constexpr int kHalves = D == 128 ? 2 : 1;  // slots of a block
     static constexpr int kSlots = D == 32 ? 4 : (kCtas == 3 ? 2 : 3);
     static constexpr bool kQueriesInSmem = NT > 1;  // a warp prepares a row tile; else each the only one, in registers
@@ -120,11 +125,11 @@ struct Parts {
     float *lb;     // [B * Hkv][blocks][R]
 };
 
-template <int D, int NT>
+template <int D, int NT, int Ctas>
 struct Smem {
     static constexpr int kRows = 8 * NT;
-    static constexpr int kSlots = Cfg<D, NT>::kSlots;
-    static constexpr int kSlot = 2 * kBlock * D / Cfg<D, NT>::kHalves;
+    static constexpr int kSlots = Cfg<D, NT, Ctas>::kSlots;
+    static constexpr int kSlot = 2 * kBlock * D / Cfg<D, NT, Ctas>::kHalves;
     static constexpr int kPitch = D + 4;  // rows of partial outputs: four rows apart are on other banks
     // the rings; once they are empty, the warps' outputs and then the CTA's
     union {
@@ -134,7 +139,7 @@ struct Smem {
             float o[kRows][D];
         };
     };
-    uint2 q[Cfg<D, NT>::kQueriesInSmem ? NT : 1][Cfg<D, NT>::kQueriesInSmem ? D / 16 : 1][32];  // fragments
+    uint2 q[Cfg<D, NT, Ctas>::kQueriesInSmem ? NT : 1][Cfg<D, NT, Ctas>::kQueriesInSmem ? D / 16 : 1][32];  // fragments
     float down[kRows];  // their rows' factors
     int seen[kRows];    // and the last position each sees
     uint64_t full[kWarps][kSlots];
@@ -505,12 +510,12 @@ __device__ __forceinline__ void write_weight(const DecodeArgs &a, long long bh, 
     }
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) decode_kernel(const __grid_constant__ DecodeArgs a) {
-    using Sm = Smem<D, NT>;
-    constexpr int SL = Sm::kSlots, kRows = Sm::kRows, S = slab(D), kHalves = Cfg<D, NT>::kHalves,
-                  kAtOnce = Cfg<D, NT>::kAtOnce;
-    constexpr bool kShared = Cfg<D, NT>::kQueriesInSmem;
+template <int D, int NT, int Ctas>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT, Ctas>::kCtas) decode_kernel(const __grid_constant__ DecodeArgs a) {
+    using Sm = Smem<D, NT, Ctas>;
+    constexpr int SL = Sm::kSlots, kRows = Sm::kRows, S = slab(D), kHalves = Cfg<D, NT, Ctas>::kHalves,
+                  kAtOnce = Cfg<D, NT, Ctas>::kAtOnce;
+    constexpr bool kShared = Cfg<D, NT, Ctas>::kQueriesInSmem;
     constexpr int kSide = kBlock * D;  // bytes of a block's keys, and of its values
     static_assert(sizeof(float) * kWarps * kRows * Sm::kPitch + sizeof(float) * kRows * D <= sizeof(Sm::ring),
                   "the outputs take no more than the rings");
@@ -1077,10 +1082,6 @@ __global__ void __launch_bounds__(kJoinThreads) weight_kernel(const __grid_const
 constexpr int kRoom[3][kMaxCluster] = {{148, 148, 135, 132, 130, 132, 105, 120},
                                        {296, 296, 279, 284, 280, 270, 259, 264},
                                        {444, 444, 426, 416, 410, 426, 392, 384}};
-template <int D>
-constexpr int ctas_on_sm(int nt) {
-    return nt == 1 ? Cfg<D, 1>::kCtas : nt == 2 ? Cfg<D, 2>::kCtas : Cfg<D, 4>::kCtas;
-}
 
 // Clusters (the CTAs of one, 0: none) or runs, by what each costs in the time a
 // warp takes for a block, as if every sequence filled its cache.  Clusters of n
@@ -1099,8 +1100,7 @@ constexpr int kLongRun = 100;
 struct Shares {
     int cluster, runs;
 };
-Shares shares_for(long long tiles, int D, int nt, int blocks) {
-    const int on_sm = D == 32 ? ctas_on_sm<32>(nt) : D == 64 ? ctas_on_sm<64>(nt) : ctas_on_sm<128>(nt);
+Shares shares_for(long long tiles, int on_sm, int blocks) {
     const int(&held)[kMaxCluster] = kRoom[on_sm - 1];
     int best = 1;
     long long least = 0;
@@ -1119,7 +1119,7 @@ Shares shares_for(long long tiles, int D, int nt, int blocks) {
 }
 
 struct Plan {
-    int rows, nt, tiles;
+    int rows, nt, tiles, ctas;
     Shares shares;
     bool weigh;
     long long groups;  // row groups x row tiles
@@ -1133,7 +1133,8 @@ Plan make_plan(const Q8Cache &c, int H, int Tq, int list_n, bool weight) {
     p.nt = p.rows > 16 && c.D < 128 ? 4 : p.rows > 8 ? 2 : 1;
     p.tiles = (p.rows + 8 * p.nt - 1) / (8 * p.nt);
     p.groups = (long long)c.B * c.H * (lists ? Tq : 1) * p.tiles;
-    p.shares = shares_for(p.groups, c.D, p.nt, lists ? list_n : c.blocks);  // (the kernel counts a list's places too)
+    p.ctas = ctas_on_sm(c.D, p.nt, p.groups > kRoom[1][0]);
+    p.shares = shares_for(p.groups, p.ctas, lists ? list_n : c.blocks);  // (the kernel counts a list's places too)
     p.weigh = weight && p.shares.cluster && p.tiles == 1;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     const size_t rows = p.shares.cluster ? 0 : (size_t)(p.groups + p.shares.runs) * 8 * p.nt;
@@ -1145,7 +1146,7 @@ Plan make_plan(const Q8Cache &c, int H, int Tq, int list_n, bool weight) {
     return p;
 }
 
-template <int D, int NT>
+template <int D, int NT, int Ctas>
 cudaError_t launch(const DecodeArgs &a, const Plan &p, cudaStream_t st, LaunchInfo &li) {
     int dev = 0;
     cudaError_t e;
@@ -1154,13 +1155,13 @@ cudaError_t launch(const DecodeArgs &a, const Plan &p, cudaStream_t st, LaunchIn
     // (144 row tiles of 16 blocks in 288 CTAs: 8.9 us on 127 SMs, 7.9 us with two CTAs on each).
     const size_t smem_most = 227 * 1024;
     static std::atomic<unsigned long long> smem_set{0};
-    if ((e = set_max_smem_once(reinterpret_cast<const void *>(decode_kernel<D, NT>), smem_most, dev, smem_set)) !=
+    if ((e = set_max_smem_once(reinterpret_cast<const void *>(decode_kernel<D, NT, Ctas>), smem_most, dev, smem_set)) !=
         cudaSuccess)
         return e;
     const long long grid = a.cluster ? p.groups * a.cluster : a.runs;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    size_t smem = sizeof(Smem<D, NT>) + 128;
-    for (int per = 1; per < Cfg<D, NT>::kCtas; ++per)
+    size_t smem = sizeof(Smem<D, NT, Ctas>) + 128;
+    for (int per = 1; per < Ctas; ++per)
         if (grid <= kRoom[per - 1][a.cluster ? a.cluster - 1 : 0]) {
             smem = smem_most / per / 1024 * 1024 - 1024;
             break;
@@ -1180,7 +1181,7 @@ cudaError_t launch(const DecodeArgs &a, const Plan &p, cudaStream_t st, LaunchIn
     cfg.attrs = attr;
     cfg.numAttrs = a.cluster > 1 ? 2 : 1;
     if ((e = mark_main_start(li, st)) != cudaSuccess) return e;
-    if ((e = cudaLaunchKernelEx(&cfg, decode_kernel<D, NT>, a)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, decode_kernel<D, NT, Ctas>, a)) != cudaSuccess) return e;
     li.kernels += 1;
     if ((e = mark_main_end(li, st)) != cudaSuccess) return e;
     if (!a.cluster) {
@@ -1234,16 +1235,19 @@ cudaError_t q8_decode(const Q8Cache &c, const Q8Decode &d, int *err, cudaStream_
     a.part.total = d.weight && !p.weigh ? reinterpret_cast<float *>(ws + p.total) : nullptr;
     a.part.lb = reinterpret_cast<float *>(ws + p.lb);
     a.err = err;
-#define ATTN_Q8_CASE(DD, NN) \
-    if (c.D == DD && p.nt == NN) return launch<DD, NN>(a, p, st, li);
-    ATTN_Q8_CASE(32, 1)
-    ATTN_Q8_CASE(32, 2)
-    ATTN_Q8_CASE(32, 4)
-    ATTN_Q8_CASE(64, 1)
-    ATTN_Q8_CASE(64, 2)
-    ATTN_Q8_CASE(64, 4)
-    ATTN_Q8_CASE(128, 1)
-    ATTN_Q8_CASE(128, 2)
+#define ATTN_Q8_CASE(DD, NN, CC) \
+    if (c.D == DD && p.nt == NN && p.ctas == CC) return launch<DD, NN, CC>(a, p, st, li);
+    ATTN_Q8_CASE(32, 1, 3)
+    ATTN_Q8_CASE(32, 2, 3)
+    ATTN_Q8_CASE(32, 4, 2)
+    ATTN_Q8_CASE(32, 4, 3)
+    ATTN_Q8_CASE(64, 1, 3)
+    ATTN_Q8_CASE(64, 2, 2)
+    ATTN_Q8_CASE(64, 2, 3)
+    ATTN_Q8_CASE(64, 4, 2)
+    ATTN_Q8_CASE(128, 1, 2)
+    ATTN_Q8_CASE(128, 1, 3)
+    ATTN_Q8_CASE(128, 2, 2)
 #undef ATTN_Q8_CASE
     return cudaErrorInvalidValue;
 }
