@@ -225,6 +225,14 @@ __global__ void __launch_bounds__(kThreads)
 // ---- read: positions starts[b] .. + n - 1 as they are held, in bf16 (zero
 // rows past the end).  One CTA takes one block of 64 positions.
 constexpr int kReadThreads = 256;
+// A code byte under the exponent of 2^23: the float 2^23 + code; and two of these as held numbers in bf16 (subtracting
+// 2^23 + 128 is exact).
+__device__ __forceinline__ uint32_t code_float(uint32_t w, int byte) { return __byte_perm(w, 0x4B000000u, 0x7650 | byte); }
+__device__ __forceinline__ uint32_t held_pair(uint32_t a, uint32_t b, uint64_t scale) {
+    const uint64_t x = f2pack(__uint_as_float(a), __uint_as_float(b));
+    const float2 r = f2unpack(fmul2(fadd2(x, f2pack(-8388736.f, -8388736.f)), scale));
+    return pack_bf16x2(r.x, r.y);
+}
 template <int D>
 __global__ void __launch_bounds__(kReadThreads)
     read_kernel(const Q8Cache c, const int32_t *__restrict__ lens, const int32_t *__restrict__ starts, int n,
@@ -269,7 +277,7 @@ __global__ void __launch_bounds__(kReadThreads)
             const int e = tid + i * kReadThreads, t = e / kChunks, ch = 8 * (e % kChunks);
             if (wanted(t)) kw[i] = *reinterpret_cast<const uint2 *>(kc + key_offset<D>(t, ch));
         }
-        const float ks = scale.x, vs = scale.y;
+        const uint64_t ks = f2pack(scale.x, scale.x), vs = f2pack(scale.y, scale.y);
 #pragma unroll
         for (int i = 0; i < kValues; ++i) {
             const int e = tid + i * kReadThreads, ch = e / (kBlock / 16), q = 4 * (e % (kBlock / 16));
@@ -286,10 +294,10 @@ __global__ void __launch_bounds__(kReadThreads)
             if (!wanted(t)) continue;
             const uint2 w = kw[i];
             uint4 r;
-            r.x = pack_bf16x2((int)((w.x & 255) - 128) * ks, (int)(((w.x >> 8) & 255) - 128) * ks);
-            r.y = pack_bf16x2((int)(((w.x >> 16) & 255) - 128) * ks, (int)((w.x >> 24) - 128) * ks);
-            r.z = pack_bf16x2((int)((w.y & 255) - 128) * ks, (int)(((w.y >> 8) & 255) - 128) * ks);
-            r.w = pack_bf16x2((int)(((w.y >> 16) & 255) - 128) * ks, (int)((w.y >> 24) - 128) * ks);
+            r.x = held_pair(code_float(w.x, 0), code_float(w.x, 1), ks);
+            r.y = held_pair(code_float(w.x, 2), code_float(w.x, 3), ks);
+            r.z = held_pair(code_float(w.y, 0), code_float(w.y, 1), ks);
+            r.w = held_pair(code_float(w.y, 2), code_float(w.y, 3), ks);
             *reinterpret_cast<uint4 *>(ko + (p0 + t - start) * D + ch) = r;
         }
         __syncthreads();
@@ -302,12 +310,11 @@ __global__ void __launch_bounds__(kReadThreads)
             for (int y = 0; y < 4; ++y) {
                 const long long p = p0 + 4 * quad + y;
                 if (p < first || p >= last) continue;
-                float f[8];
+                uint32_t r[4];
 #pragma unroll
-                for (int x = 0; x < 8; ++x) f[x] = (int)(((w[x] >> (8 * y)) & 255) - 128) * vs;
-                *reinterpret_cast<uint4 *>(vo + (p - start) * D + ch) =
-                    make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                               pack_bf16x2(f[6], f[7]));
+                for (int x = 0; x < 4; ++x)
+                    r[x] = held_pair(code_float(w[2 * x], y), code_float(w[2 * x + 1], y), vs);
+                *reinterpret_cast<uint4 *>(vo + (p - start) * D + ch) = make_uint4(r[0], r[1], r[2], r[3]);
             }
         }
         return;

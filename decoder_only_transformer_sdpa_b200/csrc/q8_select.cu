@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(kThreads)
     const int r = (int)(which % Tq);
     const long long bh = which / Tq;
     const int b = (int)(bh / c.H), h = (int)(bh % c.H);
-    if (ctas > 1) cg::this_cluster().barrier_arrive();  // (waited for before another CTA's shared memory is written)
+    // (waited for before another CTA's shared memory is written; nothing is passed on by it)
+    if (ctas > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     grid_dep_wait();
     grid_dep_launch();
     // ---- this lane's first blocks and query channels are on their way while the length is (within the cache, whatever
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kThreads)
     const int step = kRow * kAtOnce;
     load(rank * step, c.blocks);
     const int L = max(0, checked_length(lens[b], c.blocks, err));
-    if (ctas > 1) cg::this_cluster().barrier_wait();  // the cluster's CTAs have all started
+    if (ctas > 1) asm volatile("barrier.cluster.wait;" ::: "memory");  // the cluster's CTAs have all started
     const int last = L - Tq + r;  // the query's own position
     const int count = last < 0 ? 0 : min(L / kBlock, last / kBlock + 1);
     if (count > n) {  // (the same in all CTAs of the cluster)
