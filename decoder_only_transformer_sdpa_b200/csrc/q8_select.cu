@@ -7,7 +7,9 @@
 // order keys in shared memory and finds the n-th largest ten bits at a time,
 // from the highest bit in which any two keys differ (a histogram of the keys
 // that agree so far; starting at the top bits, which scores of one size share,
-// every key would count in one bin).
+// every key would count in one bin).  Up to 256 keys are ranked by comparing each
+// with each instead, which has two barriers and not some twelve (choice and decode
+// over 128 blocks 11.0 -> 9.9 us, eviction of 16 blocks and reading 20.8 -> 18.5).
 //
 // The score of block J for query q is a bound on its keys' products with q,
 // with q in 8 bits too: c = rint(127 q / max|q|),
