@@ -357,6 +357,28 @@ def test_decode_shared_out_by_the_lengths(D, B, H, G, tq, room):
     check_decode(q, o, lse, seqs, lens, label="lists of every block")
 
 
+@pytest.mark.parametrize("D,G,tq", [(32, 4, 8), (64, 4, 4), (64, 2, 16), (128, 8, 1), (128, 4, 4)])
+@pytest.mark.parametrize("B,room", [(31, 130), (51, 64 * 40)])
+def test_decode_more_row_tiles_than_are_taken_at_once(D, G, tq, B, room):
+    """Ten key heads a sequence: with short texts and, in equal runs, with long ones. Some sequences are checked."""
+    H = 10
+    lens = [room - (b * 37) % (room + 1) for b in range(B)]
+    lens[1], lens[-2], lens[-1] = 0, 1, 64
+    k, v = tokens(D + G + B, B, H, room, D)
+    c, L = filled(k, v, lens)
+    q = queries(B + tq, B, H * G, tq, D)
+    o, lse = A.attn_q8_decode(q.to(dev()), c, L, weight="set")
+    assert status() == 0
+    some = [0, 1, B // 2, B - 2, B - 1] if room < 1000 else [B // 2, B - 1]
+    heads = range(H) if room < 1000 else range(3, 5)
+    weight = c.weight.double().cpu().numpy()
+    for b in some:
+        seqs = [[R.Sequence(k[b, h, :lens[b]].double().numpy(), v[b, h, :lens[b]].double().numpy()) for h in heads]]
+        rows = slice(heads[0] * G, (heads[-1] + 1) * G)
+        check_decode(q[b:b + 1, rows], o[b:b + 1, rows], lse[b:b + 1, rows], seqs, [lens[b]],
+                     weight=weight[b:b + 1, heads[0]:heads[-1] + 1], label=f"sequence {b}")
+
+
 @pytest.mark.parametrize("qs,ks,vs", [(100.0, 10.0, 1.0), (1e-3, 1e-3, 1e3), (1e10, 1e-10, 1e-20), (0.0, 1.0, 1.0),
                                       (1e-30, 1e30, 1e30), (20.0, 1.0, 0.0)])
 def test_decode_magnitudes(qs, ks, vs):
