@@ -580,6 +580,30 @@ def test_select_ties_zeros_and_many_blocks():
     assert status() == 0
 
 
+@pytest.mark.parametrize("count", [2, 127, 128, 129, 200, 255, 256, 257, 511, 513])
+def test_select_and_evict_few_and_many_blocks(count):
+    """Around the counts at which blocks are chosen in another way, with ties, for several numbers kept."""
+    D = 32
+    c = A.Q8Cache.empty(2, 2, D, 64 * count, device=dev())
+    room = A.Q8Cache.empty(2, 2, D, 64 * count, device=dev())
+    g = torch.Generator().manual_seed(count)
+    level = torch.randint(0, 40, (2, 2, count), generator=g)
+    c.bounds[:, :, :, 1] = level[..., None].to(torch.int8).to(dev())
+    c.scales[..., 0] = 1.0
+    c.weight.copy_(level)
+    q = torch.ones(2, 2, 1, D, dtype=torch.bfloat16, device=dev())
+    L = ints(64 * count, 64 * count)
+    for n in sorted({1, 2, count // 3 + 1, count - 1, count}):
+        got = A.attn_q8_select(q, c, L, n)
+        _, kept = A.attn_q8_evict(c, L, n, recent=0, out=room)
+        for b in range(2):
+            for h in range(2):
+                want = R.best_of(level[b, h].numpy(), n)
+                assert got[b, h, 0].tolist() == want, (n, b, h)
+                assert kept[b, h].tolist() == want, (n, b, h)
+    assert status() == 0
+
+
 def test_sparse_lists_that_are_wrong_are_skipped_and_reported():
     lens = (64 * 6 + 9,)
     k, v = tokens(14, 1, 1, lens[0], 64)
