@@ -50,6 +50,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kPShift = 7.f;   // P is held as 2^7 exp2(s - m)
 constexpr float kSlack = 8.f;    // how far a score may pass m before m moves
+constexpr float kLeastFactor = 0x1p-126f;  // of a block's sums, for scores
 constexpr int kMaxCluster = 8;   // portable cluster size
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -801,8 +802,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Ctas>::kCtas) decode_kern
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     f[nt][x] = sc.x * factor(nt, x);
-                    // a block of zeros: any factor gives its scores 0 and keeps -inf what it is (a NaN stays)
-                    if (f[nt][x] == 0.f) f[nt][x] = 1.f;
+                    // A factor of 0 would turn -inf into NaN.  It stands for a block of zeros, or for scores below
+                    // 2^-120 (sums are below 2^29, and the factor was below 2^-149): with the smallest normal number
+                    // those stay next to nothing, -inf what it is and a NaN one.
+                    if (f[nt][x] == 0.f) f[nt][x] = kLeastFactor;
                 }
             softmax_step<D, NT, 4>(st, sv, f, sum);
             if (a.weight) {
