@@ -14,11 +14,16 @@
 // of a tile and not fifteen sixteenths; tcgen05 tiles start at 64 rows.  Codes
 // turn into f16 exactly (|code - 128| <= 127); queries are scaled by a power of
 // two that brings the row's largest value to [2^14, 2^15), which keeps all
-// eight bits of anything down to 2^-31 of it.  P is rounded to f16 (half a
-// step: 2^-11, an eighth of the bf16 output's 2^-8) as 2^7 exp(s - m) with a
-// reference m that is at most 2^8 below the running maximum, so that weights
-// down to 2^-21 of the largest keep that precision and those down to 2^-32
-// count.  Sums of P, the scores and both accumulators are float32.
+// eight bits of anything down to 2^-31 of it (where that power is at most
+// 2^114: a row whose largest value is below 2^-100 keeps eight bits down to
+// 2^-131, with errors of 2^-139 at most).  P is rounded to f16 (half a step:
+// 2^-11, an eighth of the bf16 output's 2^-8) as 2^13 exp(s - m) with a reference
+// m that is at most 2^2 below the running maximum.  Weights below 2^-27 of the
+// reference, some 19 below the largest score, would lose bits there, and they are
+// all of the output where the heavier tokens' values are zero: such a block's take
+// products of their own, 2^29 times as large for each 2^29 that they are smaller
+// (light_weights), down to where exp underflows in float32.  Sums of P, the scores
+// and both accumulators are float32.
 //
 // What bounds it is the stream of codes, 128 D bytes a block: every warp has a
 // ring of its own in shared memory, filled by bulk copies that its first lane
@@ -48,8 +53,12 @@ namespace cg = cooperative_groups;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr float kPShift = 7.f;   // P is held as 2^7 exp2(s - m)
-constexpr float kSlack = 8.f;    // how far a score may pass m before m moves
+constexpr float kPShift = 13.f;  // P is held as 2^13 exp2(s - m)
+constexpr float kSlack = 2.f;    // how far a score may pass m before m moves
+// (The two share f16's 2^15.  The more slack, the less often m moves and the more often weights are too light: 8, 3, 2
+// and 1 take 37.0, 33.9, 33.6 and 33.9 us over 16411 tokens of 4 x 8 heads of 128 with 16 rows, whose scores spread by
+// 1.8; without the light weights' check and products it were 31.8.)
+constexpr float kLeastF16 = 0x1p-14f;  // from here on f16 has its eleven bits
 constexpr float kLeastFactor = 0x1p-126f;  // of a block's sums, for scores
 constexpr int kMaxCluster = 8;   // portable cluster size
 
@@ -342,6 +351,63 @@ __device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&s)[Tiles]
             st.l[nt][x] += t;
         }
     }
+}
+
+// Adds the weights of row tile nt that f16 does not hold with all of its bits,
+// below kLeastF16, times the block's values to the outputs, and takes them out of
+// s.  Each pass has those within 2^29 of one another, times a power of two; `v`:
+// the lane's 16 tokens of channel g.  The whole warp calls it.
+template <int D, int NT>
+__device__ __forceinline__ void light_weights(State<D, NT> &st, float (&s)[4][NT][4], int nt, float scale,
+                                              const uint8_t *v) {
+    constexpr float kUp = 0x1p29f, kDown = 0x1p-29f, kMost = kLeastF16 * kUp;
+    bool some = false;  // lighter ones than those of the passes so far
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) some = some || (s[u][nt][x] > 0.f && s[u][nt][x] < kLeastF16);
+    float up = kUp, down = kDown;
+#pragma unroll 1
+    for (; __any_sync(0xffffffffu, some); up *= kUp, down *= kDown) {  // (four times at most: weights are normal numbers)
+        uint32_t p[4][2];
+        some = false;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                float w[2];
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const float x = s[u][nt][2 * y + z] * up;
+                    some = some || (x > 0.f && x < kLeastF16);
+                    w[z] = x >= kLeastF16 && x < kMost ? x : 0.f;
+                }
+                p[u][y] = transpose8(pack_f16x2(w[0], w[1]));
+            }
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(v + 16 * c * kBlock);
+            const uint4 b = *reinterpret_cast<const uint4 *>(v + (16 * c + 8) * kBlock);
+            const uint32_t r0[4] = {a.x, a.y, a.z, a.w}, r1[4] = {b.x, b.y, b.z, b.w};
+            float acc[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t va[4] = {codes_f16x2<0>(r0[u]), codes_f16x2<0>(r1[u]), codes_f16x2<1>(r0[u]),
+                                        codes_f16x2<1>(r1[u])};
+                if (u == 0)
+                    mma_f16_first(acc, va, p[u][0], p[u][1]);
+                else
+                    mma_f16(acc, va, p[u][0], p[u][1]);
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) st.o[c][nt][x] = fmaf(scale, acc[x] * down, st.o[c][nt][x]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (s[u][nt][x] < kLeastF16) s[u][nt][x] = 0.f;
 }
 
 // A load that stays where it is written, ahead of what it overlaps with.
@@ -822,6 +888,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Ctas>::kCtas) decode_kern
                                 v == 0.f ? -INFINITY : st.m[nt][x] + lg2(v);
                     }
             }
+            const uint8_t *vb = sm.ring[warp][slot] + (kHalves == 2 ? 0 : kSide) + g * kBlock + 16 * t;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float least = sv[0][nt][0];
+#pragma unroll
+                for (int x = 1; x < 16; ++x) least = fminf(least, sv[x / 4][nt][x % 4]);
+                // (a wait that runs out here does so again below)
+                if (__any_sync(0xffffffffu, least < kLeastF16) && (kHalves == 1 || wait()))
+                    light_weights<D, NT>(st, sv, nt, sc.y, vb);
+            }
             uint32_t p[4][NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -832,7 +908,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Ctas>::kCtas) decode_kern
                 }
             // O^T: channels 16 c + g and + 8, the lane's 16 tokens 16 t ..; a block's sum is scaled as it joins the rest
             if (kHalves == 2 && !(ok = wait())) break;
-            const uint8_t *vb = sm.ring[warp][slot] + (kHalves == 2 ? 0 : kSide) + g * kBlock + 16 * t;
 #pragma unroll
             for (int c0 = 0; c0 < D / 16; c0 += kAtOnce) {
                 uint32_t r0[kAtOnce][4], r1[kAtOnce][4];

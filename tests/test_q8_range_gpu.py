@@ -1,6 +1,7 @@
 """The 8-bit cache's decode where numbers of very different sizes meet:
 against the definition in 64 bits, within the bounds that
 tests/q8_reference.py derives."""
+import numpy as np
 import pytest
 import torch
 
@@ -44,3 +45,55 @@ def test_decode_blocks_of_tiny_keys_among_others(D, G, tq, qs, ks, tiny):
     o, lse = A.attn_q8_decode(q.to(dev()), c, L, blocks=blocks.to(dev()))
     assert status() == 0
     check_decode(q, o, lse, sequences(k, v, lens), lens, lists=blocks.numpy(), label=f"lists {qs} {ks} {tiny}")
+
+
+# ------------------------------ one token far above the others, worth nothing
+
+
+def sink(D, rows_q, n, at, gap, seed=0):
+    """One key head: token `at` has the score `gap` and the value 0, the others' scores lie around 0 and their values
+    around exp(gap), up to 10^26. Queries [1, Hq, Tq, D], to be used with scale 1."""
+    k, v = (torch.randn(1, 1, n, D, generator=torch.Generator().manual_seed(seed + i)) for i in range(2))
+    k[..., 0] = 0
+    k[0, 0, at] = 0
+    k[0, 0, at, 0] = gap / 8
+    v = v * min(float(np.exp(gap)), 1e26)
+    v[0, 0, at] = 0
+    q = queries(seed, 1, *rows_q, D, scale=D**-0.5)
+    q[..., 0] = 8
+    return k.to(torch.bfloat16), v.to(torch.bfloat16), q
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("rows_q", [(1, 1), (3, 4), (20, 1), (5, 8)])
+@pytest.mark.parametrize("gap", [12.0, 16.0, 20.0, 24.0, 32.0, 48.0, 80.0])
+def test_decode_tokens_far_below_one_without_a_value(D, rows_q, gap):
+    """What the softmax leaves to the other tokens is all of the output."""
+    n = 64 * 11 + 5
+    for at in (3, 64 * 6 + 63, n - 1):
+        k, v, q = sink(D, rows_q, n, at, gap)
+        for room in (n, 64 * 16000):  # in clusters, and in runs
+            c, L = filled(k, v, (n,), max_tokens=room)
+            o, lse = A.attn_q8_decode(q.to(dev()), c, L, scale=1.0, weight="set")
+            assert status() == 0
+            check_decode(q, o, lse, sequences(k, v, (n,)), (n,), scale=1.0, weight=c.weight.double().cpu().numpy(),
+                         label=f"gap {gap} at {at} room {room}")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_scores_at_many_distances(D):
+    """Every power of e from 0 to -80 below the largest, in each block, and a value's size that makes each count."""
+    n = 64 * 8
+    k, v = torch.zeros(1, 1, n, D), torch.zeros(1, 1, n, D)
+    far = (torch.arange(n) * 7 % 81).float()
+    k[0, 0, :, 0] = -far
+    v[0, 0] = torch.randn(n, D, generator=torch.Generator().manual_seed(7))
+    v[0, 0, far < 40] = 0  # the largest that counts is e^-40 of the whole
+    k, v = k.to(torch.bfloat16), (v * 1e17).to(torch.bfloat16)
+    c, L = filled(k, v, (n,))
+    q = torch.zeros(1, 2, 2, D, dtype=torch.bfloat16)
+    q[:, :, :, 0] = 1.0
+    q[:, 1] = 0.5
+    o, lse = A.attn_q8_decode(q.to(dev()), c, L, scale=1.0)
+    assert status() == 0
+    check_decode(q, o, lse, sequences(k, v, (n,)), (n,), scale=1.0, label="many distances")
