@@ -577,6 +577,26 @@ __device__ __forceinline__ void write_weight(const DecodeArgs &a, long long bh, 
     }
 }
 
+// The first block that counts at place i or a whole number of steps behind it in
+// a list out of order, and its place; -1: none.  Those count that are closed and
+// above all closed ones before them, up to the first negative entry.  The whole
+// warp calls it.
+__device__ __noinline__ int2 block_out_of_order(const int32_t *list, int i, int count, int step, int closed) {
+    for (; i < count; i += step) {
+        const int id = list[i];
+        int most = -1;
+        bool ended = id < 0;
+        for (int y = threadIdx.x & 31; y < i; y += 32) {
+            const int other = list[y];
+            ended = ended || other < 0;
+            if (other < closed) most = max(most, other);
+        }
+        if (__any_sync(0xffffffffu, ended)) break;
+        if (id < closed && id > __reduce_max_sync(0xffffffffu, most)) return make_int2(id, i);
+    }
+    return make_int2(-1, i);
+}
+
 template <int D, int NT, int Ctas>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Ctas>::kCtas) decode_kernel(const __grid_constant__ DecodeArgs a) {
     using Sm = Smem<D, NT, Ctas>;
@@ -653,18 +673,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Ctas>::kCtas) decode_kern
         const uint8_t *kc = a.c.k_codes + w.bh * a.c.blocks * (long long)(kBlock * D);
         const uint8_t *vc = a.c.v_codes + w.bh * a.c.blocks * (long long)(kBlock * D);
         const float2 *scales = reinterpret_cast<const float2 *>(a.c.scales) + w.bh * a.c.blocks;
-        // The first block at place i or a whole number of steps behind it, or -1.  What is not an ascending list of
-        // closed blocks ended by -1 is recorded, and the entry skipped.
+        // Whether the list, as far as this CTA's places go, is one of ascending closed blocks ended by negative entries
+        bool in_order = true;
+        if (list) {
+#pragma unroll 4
+            for (int i = tid; i < count; i += kThreads) {
+                const int id = list[i], before = i > 0 ? list[i - 1] : -1;
+                if (id >= 0 && (id >= closed || id <= before || (i > 0 && before < 0))) in_order = false;
+            }
+            if (!in_order) atomicExch(a.err, kErrLength);
+            in_order = __syncthreads_and(in_order);
+        }
+        // The first block at place i or a whole number of steps behind it, or -1.
         auto block_from = [&](int &i) -> int {
             if (!list) return i < count ? i : -1;
-            for (; i < count; i += step) {
-                const int id = list[i];
-                if (id < 0) continue;
-                const int before = i > 0 ? list[i - 1] : -1;
-                if (id < closed && id > before && !(i > 0 && before < 0)) return id;
-                if (lane == 0) atomicExch(a.err, kErrLength);
-            }
-            return -1;
+            if (in_order) return i < count ? max(list[i], -1) : -1;
+            const int2 found = block_out_of_order(list, i, count, step, closed);
+            i = found.y;
+            return found.x;
         };
 
         // ---- bulk copies run SL slots ahead of what is read: first 16 tokens of the open block, then the blocks

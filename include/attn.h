@@ -351,8 +351,10 @@ int attn_q8_read(const attn_q8_cache *cache, const int32_t *lens, const int32_t 
  * blocks, blocks_n: int32 [B, cache H, Tq, blocks_n] on the device, as
  *   attn_q8_select writes it: for each key head and query the closed blocks to
  *   attend to, ascending, -1 behind the last.  The open block is always
- *   attended to.  Entries out of order or not closed are skipped
- *   (ATTN_ERR_LENGTH from attn_device_error()).  NULL and 0: every block.
+ *   attended to.  What is not such a list is one with ATTN_ERR_LENGTH from
+ *   attn_device_error(): of its entries those count that are closed blocks
+ *   above every closed one before them, up to the first negative entry, so
+ *   that no block counts twice.  NULL and 0: every block.
  * weight: ATTN_Q8_WEIGHT_SET or _ADD: cache->weight of each closed block
  *   becomes (or grows by) the attention weight that this call's queries gave
  *   its tokens, summed over the queries and the heads that share the key

@@ -1,12 +1,12 @@
-"""The 8-bit cache's decode where numbers of very different sizes meet:
-against the definition in 64 bits, within the bounds that
+"""The 8-bit cache's decode where numbers of very different sizes meet, and over
+lists out of order: against the definition in 64 bits, within the bounds that
 tests/q8_reference.py derives."""
 import numpy as np
 import pytest
 import torch
 
 import decoder_only_transformer_sdpa_b200 as A
-from tests.test_q8_gpu import check_decode, dev, filled, queries, sequences, status, tokens
+from tests.test_q8_gpu import E_LENGTH, check_decode, dev, filled, queries, sequences, status, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +97,47 @@ def test_decode_scores_at_many_distances(D):
     o, lse = A.attn_q8_decode(q.to(dev()), c, L, scale=1.0)
     assert status() == 0
     check_decode(q, o, lse, sequences(k, v, (n,)), (n,), scale=1.0, label="many distances")
+
+
+# ------------------------------------------------------ lists out of order
+
+
+def taken(given, closed):
+    """The entries that count: closed blocks above every one before them, up to the first negative entry."""
+    out = []
+    for x in given:
+        if x < 0:
+            break
+        if x < closed and (not out or x > out[-1]):
+            out.append(x)
+    return out
+
+
+@pytest.mark.parametrize("D,G", [(64, 1), (32, 9), (128, 20)])
+def test_sparse_entries_count_once_whatever_came_before_them(D, G):
+    closed = 40
+    n = 64 * closed + 9
+    k, v = tokens(14 + D, 1, 1, n, D)
+    q = queries(6, 1, G, 2, D)
+    seqs = sequences(k, v, (n,))
+    g = np.random.default_rng(5)
+    lists = [[3, 5, 4, 5], [0, 7, 2, 7, 7, 3, 8], [39, 0, 1, 2, 39], [41, 3, 3, 4], [-1, 3, 4, 5], [2, -1, 3, -1, 4],
+             [5, -7, 6], [9] * 11, [*range(20), *range(10, 30)], [1, 2**31 - 1, 2, 40, 3], [*range(40), 40, 41, *range(40)],
+             [int(x) for x in g.integers(0, 44, 300)], [*range(0, 40, 2)] + [-1] * 200 + [5]]
+    for room in (closed + 1, 20000):  # in clusters, and (long lists) in runs
+        c, L = filled(k, v, (n,), max_tokens=64 * room)
+        for given in lists:
+            width = max(len(given), 4, 30000 if room > 1000 else 0)
+            both = torch.full((1, 1, 2, width), -1, dtype=torch.int32)
+            both[0, 0, 0, :len(given)] = torch.tensor(given, dtype=torch.int64).int()
+            both[0, 0, 1, :4] = torch.tensor([0, 1, 30, 39])  # another token's list in order
+            o, lse = A.attn_q8_decode(q.to(dev()), c, L, blocks=both.to(dev()))
+            assert status() == E_LENGTH, given
+            want = np.full((1, 1, 2, closed), -1)
+            counts = taken(given, closed)
+            want[0, 0, 0, :len(counts)] = counts
+            want[0, 0, 1, :4] = [0, 1, 30, 39]
+            check_decode(q, o, lse, seqs, (n,), lists=want, label=str(given[:12]))
+        o, lse = A.attn_q8_decode(q.to(dev()), c, L, blocks=torch.arange(40, dtype=torch.int32).expand(1, 1, 2, 40).contiguous().to(dev()))
+        assert status() == 0
+        check_decode(q, o, lse, seqs, (n,), label="every block")
