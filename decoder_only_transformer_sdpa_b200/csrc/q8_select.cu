@@ -168,9 +168,11 @@ __device__ void largest(const uint32_t *key, int count, int n, int32_t *list, Se
     }
 }
 
-// ---- by score.  One cluster a key head and new token.
+// ---- by score.  One cluster a key head and new token.  64 registers a thread, so
+// that an SM holds two CTAs (at 84 it held one: 384 lists of 2048 blocks 35.1 us,
+// now 28.2).
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     select_kernel(const Q8Cache c, const __nv_bfloat16 *__restrict__ q, const TStrides sq,
                   const int32_t *__restrict__ lens, int32_t *__restrict__ lists, int n, int G, int Tq, int ctas,
                   int *err) {
@@ -434,9 +436,11 @@ cudaError_t q8_select(const Q8Cache &c, const __nv_bfloat16 *q, const TStrides &
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const size_t smem = ((size_t)c.blocks + 2 * (size_t)G * (c.D / 4) + G) * 4;
     // CTAs of a cluster: a step of 512 threads takes 16 D^-1 * 512 * 4 blocks; as many as there are steps, while the
-    // GPU's 148 SMs have room for two CTAs each.
+    // GPU's 148 SMs have one for each CTA (an SM holds two, so every cluster finds room at once).  Against clusters
+    // that fill two CTAs an SM (us, 148 / 259 CTAs): 96 lists of 2048 blocks 10.2 / 11.4, 64 of 8 heads of 128
+    // channels 16.3 / 17.9, 144 10.4 / 10.4, 48 10.7 / 9.2.
     const int step = kThreads / (c.D / 16) * 4;
-    int ctas = (int)(2 * 148 / grid);
+    int ctas = (int)(148 / grid);
     ctas = ctas > kMaxCluster ? kMaxCluster : ctas < 1 ? 1 : ctas;
     if (ctas > (c.blocks + step - 1) / step) ctas = (c.blocks + step - 1) / step;
     const void *fn = c.D == 32 ? (const void *)select_kernel<32>
