@@ -30,10 +30,6 @@ if not os.path.exists(LIB_PATH):
         f"{LIB_PATH} is not built; run `python decoder_only_transformer_sdpa_b200/build.py` "
         "(nvcc, sm_100a). There is no fallback implementation.")
 
-if not os.path.exists(os.path.join(_HERE, "_q8.so")):
-    raise ImportError(
-        f"{os.path.join(_HERE, '_q8.so')} is not built; run `python decoder_only_transformer_sdpa_b200/build.py`.")
-
 _lib = ctypes.CDLL(LIB_PATH)
 
 _vp, _fp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -556,6 +552,10 @@ def _binding():
     global _q8
     if _q8 is None:
         _torch()
+        if not os.path.exists(os.path.join(_HERE, "_q8.so")):
+            raise ImportError(
+                f"{os.path.join(_HERE, '_q8.so')} is not built; run `python decoder_only_transformer_sdpa_b200/build.py` "
+                "(g++, torch's headers). There is no fallback implementation.")
         module = importlib.import_module("._q8", __name__)
         module.bind(AttnError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
             _lib.attn_q8_append, _lib.attn_q8_read, _lib.attn_q8_decode_workspace_bytes, _lib.attn_q8_decode,
