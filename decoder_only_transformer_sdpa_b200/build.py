@@ -5,8 +5,8 @@ repository).  Run ``python decoder_only_transformer_sdpa_b200/build.py``
 ``--debug`` builds ``libattn_debug.so`` instead: the same kernels with the
 device-side bounds checks compiled in (-DATTN_DEVICE_CHECKS); select it with
 the ATTN_LIBRARY environment variable.  ``_q8.so``, the Python module of the
-8-bit cache's calls, is host code against torch's headers, built by g++ with
-either."""
+8-bit cache's calls, is host code against torch's headers, built by g++ after
+either; the library needs neither torch nor the module."""
 from __future__ import annotations
 
 import concurrent.futures
@@ -16,6 +16,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -41,13 +42,18 @@ def _deps():
         sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(ROOT, "include", "attn.h")]
 
 
-def build_binding(force: bool = False) -> str:
-    """The module _q8 (csrc/q8_binding.cpp); torch is found but not imported."""
+def build_binding(force: bool = False) -> Optional[str]:
+    """The module _q8 (csrc/q8_binding.cpp); torch is found but not imported.
+    None without torch, where nothing could call it."""
     src, so = os.path.join(CSRC, "q8_binding.cpp"), os.path.join(HERE, "_q8.so")
     deps = [src, os.path.join(ROOT, "include", "attn.h")]
     if not force and os.path.exists(so) and all(os.path.getmtime(p) <= os.path.getmtime(so) for p in deps):
         return so
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    found = importlib.util.find_spec("torch")
+    if found is None:
+        sys.stderr.write(f"{so} is not built: it binds the 8-bit cache to torch, which is not installed\n")
+        return None
+    torch = found.submodule_search_locations[0]
     include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
     tmp = so + f".tmp{os.getpid()}"
@@ -81,7 +87,12 @@ def _compile(src: str, verbose_ptxas: bool, debug: bool = False) -> str:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False) -> str:
+    lib = _build_library(force, verbose_ptxas, debug)
     build_binding(force)
+    return lib
+
+
+def _build_library(force: bool, verbose_ptxas: bool, debug: bool) -> str:
     lib = LIB_DEBUG if debug else LIB
     if not force and up_to_date(lib):
         return lib
