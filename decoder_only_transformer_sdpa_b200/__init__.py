@@ -16,6 +16,7 @@ import ctypes
 import importlib
 import math
 import os
+import sys
 from typing import Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -557,6 +558,10 @@ def _binding():
                 f"{os.path.join(_HERE, '_q8.so')} is not built; run `python decoder_only_transformer_sdpa_b200/build.py` "
                 "(g++, torch's headers). There is no fallback implementation.")
         module = importlib.import_module("._q8", __name__)
+        here = f"torch {_torch().__version__}, {sys.implementation.cache_tag}"
+        if module.built_for != here:
+            raise ImportError(f"_q8.so is built for {module.built_for}, this is {here}; "
+                              "run `python decoder_only_transformer_sdpa_b200/build.py`.")
         module.bind(AttnError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
             _lib.attn_q8_append, _lib.attn_q8_read, _lib.attn_q8_decode_workspace_bytes, _lib.attn_q8_decode,
             _lib.attn_q8_select, _lib.attn_q8_evict_workspace_bytes, _lib.attn_q8_evict)))

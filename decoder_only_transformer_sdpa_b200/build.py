@@ -13,6 +13,7 @@ import concurrent.futures
 import glob
 import importlib.util
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -42,22 +43,34 @@ def _deps():
         sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(ROOT, "include", "attn.h")]
 
 
+def _torch_version(folder: str) -> str:
+    """The version that the torch installed there reports, by its version.py alone."""
+    with open(os.path.join(folder, "version.py")) as f:
+        return re.search(r"^__version__ = ['\"]([^'\"]+)['\"]", f.read(), re.M).group(1)
+
+
 def build_binding(force: bool = False) -> Optional[str]:
     """The module _q8 (csrc/q8_binding.cpp); torch is found but not imported.
-    None without torch, where nothing could call it."""
+    None without torch, where nothing could call it.  The module carries the
+    versions of torch and Python that it is built against, and is built anew for
+    others."""
     src, so = os.path.join(CSRC, "q8_binding.cpp"), os.path.join(HERE, "_q8.so")
     deps = [src, os.path.join(ROOT, "include", "attn.h")]
-    if not force and os.path.exists(so) and all(os.path.getmtime(p) <= os.path.getmtime(so) for p in deps):
-        return so
     found = importlib.util.find_spec("torch")
     if found is None:
         sys.stderr.write(f"{so} is not built: it binds the 8-bit cache to torch, which is not installed\n")
         return None
     torch = found.submodule_search_locations[0]
+    built_for = f"torch {_torch_version(torch)}, {sys.implementation.cache_tag}"
+    if not force and os.path.exists(so) and all(os.path.getmtime(p) <= os.path.getmtime(so) for p in deps):
+        with open(so, "rb") as f:
+            if f"built for {built_for}\0".encode() in f.read():
+                return so
     include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
     tmp = so + f".tmp{os.getpid()}"
-    r = subprocess.run([CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", *(f"-I{d}" for d in include),
+    r = subprocess.run([CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+                        f'-DATTN_BUILT_FOR="{built_for}"', *(f"-I{d}" for d in include),
                         src, "-o", tmp, "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
                         "-ltorch_python"], capture_output=True, text=True)
     if r.returncode != 0:

@@ -372,5 +372,9 @@ PyMODINIT_FUNC PyInit__q8() {
                                     {"bind", bind, METH_VARARGS, nullptr},
                                     {nullptr, nullptr, 0, nullptr}};
     static PyModuleDef module = {PyModuleDef_HEAD_INIT, "_q8", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
-    return PyModule_Create(&module);
+    PyObject *m = PyModule_Create(&module);
+    // build.py looks for these words in the file, the package compares them with the torch and the Python it runs in
+    static const char words[] = "built for " ATTN_BUILT_FOR;
+    if (m && PyModule_AddStringConstant(m, "built_for", words + sizeof("built for ") - 1) < 0) Py_CLEAR(m);
+    return m;
 }

@@ -47,7 +47,8 @@ def with_stub_compilers(m, tmp_path):
 
     def run(cmd, **_):
         out = cmd[cmd.index("-o") + 1]
-        open(out, "w").write(" ".join(cmd))
+        words = [x.split('"')[1] for x in cmd if x.startswith("-DATTN_BUILT_FOR")]
+        open(out, "w").write("".join(f"built for {w}\0" for w in words))
         built.append(os.path.basename(out).split(".tmp")[0])
         return subprocess.CompletedProcess(cmd, 0, "", "")
 
@@ -78,3 +79,32 @@ def test_the_library_is_there_when_the_module_fails(tmp_path, debug):
     with pytest.raises(RuntimeError, match="no headers"):
         m.build(debug=debug)
     assert os.path.exists(m.LIB_DEBUG if debug else m.LIB)
+
+
+def test_the_module_is_built_anew_for_another_torch_or_python(tmp_path, monkeypatch):
+    m = build_module()
+    built = with_stub_compilers(m, tmp_path)
+    version = m._torch_version(importlib.util.find_spec("torch").submodule_search_locations[0])
+    count = lambda: built.count("_q8.so")
+    for n in (1, 1):
+        m.build_binding()
+        assert count() == n
+    monkeypatch.setattr(m, "_torch_version", lambda folder: version + "1")
+    for n in (2, 2):
+        m.build_binding()
+        assert count() == n
+    monkeypatch.setattr(sys.implementation, "cache_tag", "cpython-300")
+    m.build_binding()
+    assert count() == 3
+
+
+def test_a_module_for_another_torch_is_not_used(monkeypatch):
+    import torch
+
+    import decoder_only_transformer_sdpa_b200 as A
+    assert A._binding().built_for == f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+    monkeypatch.setattr(A, "_q8", None)
+    monkeypatch.setattr(torch, "__version__", "0.0")
+    with pytest.raises(ImportError, match="this is torch 0.0"):
+        A._binding()
+    assert A._q8 is None
