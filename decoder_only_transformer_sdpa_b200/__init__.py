@@ -8,7 +8,8 @@ the shared library is missing, importing this package raises ImportError.
 
 Functions mirror the C entry points and take [B, H, T, D] contiguous CUDA
 tensors (bf16 for ``attn_fwd``/``attn_bwd``, float32 for the ``_f32`` pair);
-outputs may be passed in or are allocated.
+outputs may be passed in or are allocated.  They carry no autograd graph, also
+where inputs require gradients: those come from the ``attn_bwd`` calls.
 """
 from __future__ import annotations
 

@@ -3,9 +3,10 @@
 // Checks what a call gets, makes the outputs that it was not lent and hands
 // addresses, strides and the device's current stream to the entry points of
 // libattn.so.  What bounds it is the host's time: a decode of one token is 4.5 us
-// of GPU time, and issuing it takes 5.0 us from here, 2.4 us of that the launch;
-// the same steps from Python (each tensor's attributes one by one, then ctypes)
-// took 11.6 us, and the GPU waited for them.
+// of GPU time, and issuing it takes 5.6 us from here, 2.4 us of that the launch
+// and 2.8 us the two outputs (2.5 straight from the allocator, unseen by dispatch
+// modes); the same steps from Python (each tensor's attributes one by one, then
+// ctypes) took 11.6 us, and the GPU waited for them.
 //
 // The functions of libattn.so come as addresses (`bind`), so that the build of
 // it that the package has loaded is the one that runs.
@@ -13,7 +14,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/cuda/EmptyTensor.h>
+#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/DynamicTypes.h>
@@ -107,9 +108,9 @@ T *whole(PyObject *o, const char *name, at::ScalarType type, at::IntArrayRef sha
     return static_cast<T *>(t.data_ptr());
 }
 
-// A new contiguous tensor, straight from the allocator: every element of it is written by the call.
+// A new contiguous tensor, by torch's dispatcher, so that what watches a program's tensors sees it.
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int index) {
-    return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, (c10::DeviceIndex)index), std::nullopt);
+    return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)index));
 }
 
 // The same, made where it is not lent; `kept` holds a reference to it.
