@@ -5,6 +5,8 @@
 
 #include <math.h>
 
+#include <array>
+
 #define ATTN_API extern "C" __attribute__((visibility("default")))
 
 using namespace attn;
@@ -13,9 +15,21 @@ namespace {
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-bool overlap(const void *a, size_t an, const void *b, size_t bn) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + bn && y < x + an;
+// A piece of memory (NULL: none) and its bytes.
+struct Part {
+    const void *at;
+    size_t bytes;
+};
+bool overlap(const Part &a, const Part &b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return x && y && x < y + b.bytes && y < x + a.bytes;
+}
+// A cache's seven parts.
+std::array<Part, 7> parts_of(const Q8Cache &c) {
+    const size_t heads = (size_t)c.B * c.H, blocks = heads * c.blocks, side = (size_t)kQ8Block * c.D;
+    const size_t ring = heads * 2 * side * sizeof(__nv_bfloat16);
+    return {{{c.k_codes, blocks * side}, {c.v_codes, blocks * side}, {c.scales, blocks * 8}, {c.bounds, blocks * 2 * c.D},
+             {c.weight, blocks * 4}, {c.recent_k, ring}, {c.recent_v, ring}}};
 }
 
 bool strides_ok(const attn_strides &x) {
@@ -206,16 +220,10 @@ ATTN_API int attn_q8_evict(const attn_q8_cache *cache, const attn_q8_cache *out,
     for (bool s : same)
         if (s != same[0]) return ATTN_ERR_OPTION;
     if (same[0] && (c.blocks != d.blocks || c.bounds != d.bounds)) return ATTN_ERR_OPTION;
-    if (!same[0]) {
-        const size_t blocks = (size_t)c.B * c.H * c.blocks, to = (size_t)d.B * d.H * d.blocks, side = (size_t)kQ8Block * c.D;
-        const size_t ring = (size_t)c.B * c.H * 2 * side * sizeof(__nv_bfloat16);
-        if (overlap(c.k_codes, blocks * side, d.k_codes, to * side) ||
-            overlap(c.v_codes, blocks * side, d.v_codes, to * side) ||
-            overlap(c.scales, blocks * 8, d.scales, to * 8) || overlap(c.recent_k, ring, d.recent_k, ring) ||
-            overlap(c.recent_v, ring, d.recent_v, ring) || (d.weight && overlap(c.weight, blocks * 4, d.weight, to * 4)) ||
-            (d.bounds && overlap(c.bounds, blocks * 2 * c.D, d.bounds, to * 2 * c.D)))
-            return ATTN_ERR_OPTION;
-    }
+    if (!same[0])
+        for (const Part &x : parts_of(c))
+            for (const Part &y : parts_of(d))
+                if (overlap(x, y)) return ATTN_ERR_OPTION;
     if (!aligned(lens, 4) || !aligned(lens_out, 4) || !aligned(kept, 4)) return ATTN_ERR_ALIGN;
     if (lens_out == lens &&
         (!workspace || workspace_bytes < attn_q8_evict_workspace_bytes(cache) || !aligned(workspace, 256)))

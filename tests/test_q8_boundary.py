@@ -153,6 +153,20 @@ def test_evict_refusals(kw, expect):
     assert evict(**kw) == expect
 
 
+PARTS = dict(k_codes=2 * 3 * 4 * 64 * 64, v_codes=2 * 3 * 4 * 64 * 64, scales=2 * 3 * 4 * 8, bounds=2 * 3 * 4 * 128,
+             weight=2 * 3 * 4 * 4, recent_k=2 * 3 * 128 * 64 * 2, recent_v=2 * 3 * 128 * 64 * 2)  # bytes of cache()
+
+
+@pytest.mark.parametrize("part", PARTS)
+@pytest.mark.parametrize("other", PARTS)
+def test_evict_refuses_to_share_memory_in_any_part(part, other):
+    """Part `part` of the target at the first byte of part `other` of the source, at its last 16, and behind it (these
+    calls lack a workspace, so that none gets any further)."""
+    at, n = getattr(cache(), other), PARTS[other]
+    for off, expect in ((0, E_OPTION), (n - 16, E_OPTION), ((n + 15) // 16 * 16, E_WS)):
+        assert evict(out=cache(**{**OTHER, part: at + off}), ws=None) == expect
+
+
 def test_workspace_sizes():
     up = lambda x: (x + 255) // 256 * 256
     c = cache(B=7, H=30, blocks=100)
