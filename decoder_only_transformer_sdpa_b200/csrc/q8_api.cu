@@ -228,6 +228,11 @@ ATTN_API int attn_q8_evict(const attn_q8_cache *cache, const attn_q8_cache *out,
     if (lens_out == lens &&
         (!workspace || workspace_bytes < attn_q8_evict_workspace_bytes(cache) || !aligned(workspace, 256)))
         return ATTN_ERR_WORKSPACE;
+    // The lengths are read while the list of kept blocks and the new lengths are written.
+    const size_t lens_bytes = (size_t)c.B * 4;
+    const Part old_lens{lens, lens_bytes}, new_lens{lens_out, lens_bytes}, list{kept, (size_t)c.B * c.H * keep * 4};
+    if ((lens_out != lens && overlap(new_lens, old_lens)) || overlap(list, old_lens) || overlap(list, new_lens))
+        return ATTN_ERR_OPTION;
     int *err = nullptr;
     if ((st = device_setup(&err)) != ATTN_OK) return st;
     return finish(q8_evict(c, d, lens, lens_out, kept, keep, sink, recent, workspace, err, stream, li),

@@ -413,14 +413,15 @@ size_t attn_q8_evict_workspace_bytes(const attn_q8_cache *cache);
  * recent <= keep).  The kept blocks move to the front in order, with scales,
  * bounds and weight, of `out`: the same cache (the same pointers), or another
  * one that shares no memory with it and holds at least min(keep, blocks)
- * blocks.  lens_out [B] (may be lens) gets the new lengths: min(closed, keep)
- * * 64 + lens[b] % 64; kept int32 [B, H, keep] the places the blocks came from,
- * ascending, -1 behind the last.  Heads keep different blocks, all of them
- * equally many.  The bf16 positions go along unchanged: where the last block
- * does not stay in every head (recent 0), lens may not fall into it, nor an
- * append before it be repeated, until 64 tokens more are there.  workspace: as
- * attn_q8_evict_workspace_bytes, 256-byte aligned, where lens_out is lens; else
- * it is not looked at.  Two launches. */
+ * blocks.  lens_out [B] (lens, or apart from it) gets the new lengths:
+ * min(closed, keep) * 64 + lens[b] % 64; kept int32 [B, H, keep] (apart from
+ * both) the places the blocks came from, ascending, -1 behind the last.
+ * Memory that overlaps in another way is ATTN_ERR_OPTION.  Heads keep different
+ * blocks, all of them equally many.  The bf16 positions go along unchanged:
+ * where the last block does not stay in every head (recent 0), lens may not fall
+ * into it, nor an append before it be repeated, until 64 tokens more are there.
+ * workspace: as attn_q8_evict_workspace_bytes, 256-byte aligned, where lens_out
+ * is lens; else it is not looked at.  Two launches. */
 int attn_q8_evict(const attn_q8_cache *cache, const attn_q8_cache *out, const int32_t *lens,
                   int32_t *lens_out, int32_t *kept, int keep, int sink, int recent, void *workspace,
                   size_t workspace_bytes, cudaStream_t stream);

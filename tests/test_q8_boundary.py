@@ -167,6 +167,13 @@ def test_evict_refuses_to_share_memory_in_any_part(part, other):
         assert evict(out=cache(**{**OTHER, part: at + off}), ws=None) == expect
 
 
+@pytest.mark.parametrize("kw", [dict(lens_out=20 * P + 4), dict(lens_out=20 * P - 4), dict(kept=20 * P), dict(kept=20 * P - 44),
+                                dict(kept=20 * P + 4), dict(lens_out=22 * P, kept=22 * P + 4), dict(lens_out=20 * P, kept=20 * P)])
+def test_evict_refuses_lengths_and_lists_that_overlap(kw):
+    """2 sequences' lengths, and 2 x 3 heads' lists of 2; nothing beyond the checks runs."""
+    assert evict(**{**dict(lens=20 * P, lens_out=20 * P, kept=21 * P), **kw}) == E_OPTION
+
+
 def test_workspace_sizes():
     up = lambda x: (x + 255) // 256 * 256
     c = cache(B=7, H=30, blocks=100)
