@@ -58,6 +58,9 @@ constexpr float kSlack = 2.f;    // how far a score may pass m before m moves
 // (The two share f16's 2^15.  The more slack, the less often m moves and the more often weights are too light: 8, 3, 2
 // and 1 take 37.0, 33.9, 33.6 and 33.9 us over 16411 tokens of 4 x 8 heads of 128 with 16 rows, whose scores spread by
 // 1.8; without the light weights' check and products it were 31.8.)
+// Outputs are summed as 2^7 exp2(s - m) times the values, so that values of 10^30 do not overflow over 10^5 tokens of one
+// weight; smaller sums would cost bits where a block's value scale is next to underflow (10^-35 keeps 16 of them).
+constexpr float kOutputs = 0x1p-6f;  // of what P gives
 constexpr float kLeastF16 = 0x1p-14f;  // from here on f16 has its eleven bits
 constexpr float kLeastFactor = 0x1p-126f;  // of a block's sums, for scores
 constexpr int kMaxCluster = 8;   // portable cluster size
@@ -491,6 +494,8 @@ __device__ __forceinline__ void open_tokens(State<D, NT> &st, float qscale, Quer
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
+            s[0][nt][2 * y] *= kOutputs;
+            s[0][nt][2 * y + 1] *= kOutputs;
             const uint32_t h = pack_bf16x2(s[0][nt][2 * y], s[0][nt][2 * y + 1]);
             const float2 r = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&h));
             b[nt][y] = transpose8(h);
@@ -553,7 +558,7 @@ __device__ __forceinline__ void write_lse(const DecodeArgs &a, const Where &w, i
     if (a.part.total) a.part.total[w.bh * (a.tiles * a.tile_rows) + r] = row_total(m, l);
 }
 // What a row's sums are multiplied by; nothing seen: zeros.
-__device__ __forceinline__ float row_factor(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float row_factor(float l) { return l == 0.f ? 0.f : 1.f / (kOutputs * l); }
 __device__ __forceinline__ void write_four(__nv_bfloat16 *to, const float4 &o, float by) {
     *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16x2(o.x * by, o.y * by), pack_bf16x2(o.z * by, o.w * by));
 }
@@ -914,6 +919,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Ctas>::kCtas) decode_kern
                                 v == 0.f ? -INFINITY : st.m[nt][x] + lg2(v);
                     }
             }
+            const float vscale = sc.y * kOutputs;
             const uint8_t *vb = sm.ring[warp][slot] + (kHalves == 2 ? 0 : kSide) + g * kBlock + 16 * t;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -922,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Ctas>::kCtas) decode_kern
                 for (int x = 1; x < 16; ++x) least = fminf(least, sv[x / 4][nt][x % 4]);
                 // (a wait that runs out here does so again below)
                 if (__any_sync(0xffffffffu, least < kLeastF16) && (kHalves == 1 || wait()))
-                    light_weights<D, NT>(st, sv, nt, sc.y, vb);
+                    light_weights<D, NT>(st, sv, nt, vscale, vb);
             }
             uint32_t p[4][NT][2];
 #pragma unroll
@@ -965,7 +971,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Ctas>::kCtas) decode_kern
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
-                            st.o[c0 + c][nt][x] = fmaf(sc.y, acc[c][nt][x], st.o[c0 + c][nt][x]);
+                            st.o[c0 + c][nt][x] = fmaf(vscale, acc[c][nt][x], st.o[c0 + c][nt][x]);
             }
             next();
             at = at_next;

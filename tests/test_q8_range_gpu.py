@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import decoder_only_transformer_sdpa_b200 as A
+from tests import q8_reference as R
 from tests.test_q8_gpu import E_LENGTH, check_decode, dev, filled, queries, sequences, status, tokens
 
 pytestmark = pytest.mark.gpu
@@ -97,6 +98,32 @@ def test_decode_scores_at_many_distances(D):
     o, lse = A.attn_q8_decode(q.to(dev()), c, L, scale=1.0)
     assert status() == 0
     check_decode(q, o, lse, sequences(k, v, (n,)), (n,), scale=1.0, label="many distances")
+
+
+# ----------------------------------------------------- very large and small values
+
+
+@pytest.mark.parametrize("size,n,room", [(1e30, 102409, 102409), (1e30, 102409, 64 * 30000), (1e30, 50, 50), (1e-30, 500, 500),
+                                         (1e-33, 500, 64 * 16000), (1e-35, 700, 700)])
+@pytest.mark.parametrize("D", [32, 128])
+def test_decode_values_near_the_ends_of_float32(D, size, n, room):
+    """Sums over many tokens of one weight stay finite, and small values keep their bits."""
+    if D == 128 and n > 1000:
+        n = room = 64 * 700 + 9
+    g = torch.Generator().manual_seed(5)
+    k = (torch.randn(1, 1, n, D, generator=g) * 0.1).to(torch.bfloat16)
+    v = ((torch.rand(1, 1, n, D, generator=g) / 2 + 0.5) * size).to(torch.bfloat16)
+    c, L = filled(k, v, (n,), max_tokens=room)
+    q = queries(8, 1, 2, 1, D, scale=0.1)
+    o, lse = A.attn_q8_decode(q.to(dev()), c, L)
+    assert status() == 0
+    s = sequences(k, v, (n,))[0][0]
+    for h in range(2):
+        row = q[0, h, 0].double().numpy()
+        eo, el, _, a_max, s_max, pv = R.attend(row, s.held_k, s.held_v, np.ones(n, bool), D**-0.5)
+        to, tl, _ = R.tolerances(D, s.closed, D**-0.5, row, s.held_k, a_max, s_max, eo, el, pv)
+        assert np.all(np.abs(o[0, h, 0].double().cpu().numpy() - eo) <= to - 1e-30 + 2.0**-133)  # (the smallest bf16)
+        assert abs(float(lse[0, h, 0]) - el) <= tl
 
 
 # ------------------------------------------------------ lists out of order
