@@ -434,7 +434,7 @@ cudaError_t q8_select(const Q8Cache &c, const __nv_bfloat16 *q, const TStrides &
     const int G = H / c.H;
     const long long grid = (long long)c.B * c.H * Tq;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const size_t smem = ((size_t)c.blocks + 2 * (size_t)G * (c.D / 4) + G) * 4;
+    size_t smem = ((size_t)c.blocks + 2 * (size_t)G * (c.D / 4) + G) * 4;
     // CTAs of a cluster: a step of 512 threads takes 16 D^-1 * 512 * 4 blocks; as many as there are steps, while the
     // GPU's 148 SMs have one for each CTA (an SM holds two, so every cluster finds room at once).  Against clusters
     // that fill two CTAs an SM (us, 148 / 259 CTAs): 96 lists of 2048 blocks 10.2 / 11.4, 64 of 8 heads of 128
@@ -443,6 +443,11 @@ cudaError_t q8_select(const Q8Cache &c, const __nv_bfloat16 *q, const TStrides &
     int ctas = (int)(148 / grid);
     ctas = ctas > kMaxCluster ? kMaxCluster : ctas < 1 ? 1 : ctas;
     if (ctas > (c.blocks + step - 1) / step) ctas = (c.blocks + step - 1) / step;
+    // CTAs fill one SM after another, so where each has one it asks for more than half of the shared memory: a decode
+    // that follows starts where the choice leaves room, and else finds its clusters crowded onto the SMs without one
+    // (choice and decode of 64 lists of 128 channels 23.9 us, now 21.2; of 96 over up to 2048 blocks 30.7, now 27.6).
+    const size_t more_than_half = 120 * 1024;
+    if (grid * ctas <= 148 && smem < more_than_half) smem = more_than_half;
     const void *fn = c.D == 32 ? (const void *)select_kernel<32>
                                : c.D == 64 ? (const void *)select_kernel<64> : (const void *)select_kernel<128>;
     int dev = 0;
