@@ -53,15 +53,15 @@ namespace cg = cooperative_groups;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr float kPShift = 13.f;  // P is held as 2^13 exp2(s - m)
-constexpr float kSlack = 2.f;    // how far a score may pass m before m moves
-// (The two share f16's 2^15.  The more slack, the less often m moves and the more often weights are too light: 8, 3, 2
-// and 1 take 37.0, 33.9, 33.6 and 33.9 us over 16411 tokens of 4 x 8 heads of 128 with 16 rows, whose scores spread by
-// 1.8; without the light weights' check and products it were 31.8.)
-// Outputs are summed as 2^7 exp2(s - m) times the values, so that values of 10^30 do not overflow over 10^5 tokens of one
-// weight; smaller sums would cost bits where a block's value scale is next to underflow (10^-35 keeps 16 of them).
-constexpr float kOutputs = 0x1p-6f;  // of what P gives
-constexpr float kLeastF16 = 0x1p-14f;  // from here on f16 has its eleven bits
+// P is held as 2^13 exp2(s - m), and a score may pass m by 2 before m moves: the two share f16's 2^15.  The more slack,
+// the less often m moves and the more often weights are too light (below kLeastF16 = 2^-14, from where on f16 has its
+// eleven bits): 8, 3, 2 and 1 take 37.0, 33.9, 33.6 and 33.9 us over 16411 tokens of 4 x 8 heads of 128 with 16 rows,
+// whose scores spread by 1.8; without the light weights' check and products it were 31.8.
+constexpr float kPShift = 13.f, kSlack = 2.f, kLeastF16 = 0x1p-14f;
+// Outputs are summed as 2^7 exp2(s - m) times the values (what P gives times kOutputs), so that values of 10^30 do not
+// overflow over 10^5 tokens of one weight; smaller sums would cost bits where a block's value scale is next to underflow
+// (10^-35 keeps 16 of them).
+constexpr float kOutputs = 0x1p-6f;
 constexpr float kLeastFactor = 0x1p-126f;  // of a block's sums, for scores
 constexpr int kMaxCluster = 8;   // portable cluster size
 
@@ -105,11 +105,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // Warps of a CTA, slots of a warp's ring (a block, or half of one at D = 128),
 // and CTAs that an SM holds: three of 168 registers a thread, or two of 255 where
 // the sums take more.  In between (32 rows of 32 channels, 16 of 64, 8 of 128),
-// where three CTAs spill 40 to 140 bytes a thread, three only where two would
-// leave row tiles waiting.  Us with three / two: 16 rows of 64, 432 row tiles 23.5
-// / 57, 273 short ones 8.2 / 8.0, 6 long ones 13.1 / 11.8; 32 rows of 32, 400 row
-// tiles 16.5 / 25.1; 8 rows of 128, 400 row tiles of 100 tokens 7.5 / 11.0 and of
-// 2000 tokens 41.4 / 40.6, 128 of up to 16384 tokens 64.6 / 59.4.
+// where three CTAs spill 30 to 80 bytes a thread, three only where two would
+// leave row tiles waiting.  Us with three / two: 16 rows of 64, 432 row tiles of
+// 2000 tokens 27.5 / 42.5, 273 of 300 tokens 8.3 / 8.2, 6 of 17000 13.6 / 12.7; 32
+// rows of 32, 400 row tiles of 1000 tokens 18.9 / 28.2; one row of 128, 400 row
+// tiles of 100 tokens 7.7 / 11.6 and of 2000 tokens 38.3 / 42.0, 128 of up to 16384
+// tokens 61.3 / 60.8.
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int ctas_on_sm(int D, int nt, bool crowded) {
@@ -305,9 +306,9 @@ struct State {
 
 // Folds the scores f * s[i][nt] (log2 units, f >= 0; s = -inf where masked) of
 // 16 * Tiles tokens into the running softmax and replaces them by
-// 2^7 exp2(f s - m); the sums of this lane's weights go to `sum`.  The
+// 2^13 exp2(f s - m); the sums of this lane's weights go to `sum`.  The
 // reference m moves (to the maximum so far) only when a score passes it by more
-// than kSlack, which after the first blocks hardly happens: one vote a block
+// than kSlack, which after the first blocks is rare: one vote a block
 // instead of two butterflies.
 template <int D, int NT, int Tiles>
 __device__ __forceinline__ void softmax_step(State<D, NT> &st, float (&s)[Tiles][NT][4], const float (&f)[NT][2],
@@ -1198,14 +1199,15 @@ constexpr int kRoom[3][kMaxCluster] = {{148, 148, 135, 132, 130, 132, 105, 120},
 // CTAs a row tile: the rounds that the GPU needs for all of them times the blocks
 // a warp reads and kPerCta beside them.  Runs: each warp's even share of all units
 // and kPerRuns for finding them and joining what they leave.  Measured (us,
-// clusters / runs; row tiles x blocks): 144 x 16 7.9 / 9.6, 200 x 64 22 / 23,
-// 32 x 257 (head size 128, 16 rows) 33 / 37, 432 x 24 (16 rows) 22 / 46, 6 x 265
-// (16 rows) 17 / 14.5, 1 x 2048 66 / 22, 192 x up to 512 98 / 84.  Runs where the
+// clusters / runs; row tiles x blocks): 144 x 16 8.1 / 11.8, 200 x up to 64 with
+// weights 22.1 / 23.1, 32 x 257 (head size 128, 16 rows) 33.9 / 36.1, 432 x 24 (16
+// rows) 22.7 / 51.5, 6 x 265 (16 rows) 17.8 / 12.7, 1 x 2048 69.3 / 12.0, 192 x up
+// to 512 99.8 / 84.5.  Runs where the
 // two come out alike: unequal lengths, which they even out, cost clusters more.
 constexpr int kPerCta = 3, kPerRuns = 5;
 // Where a run is long, two for each CTA that the GPU holds let an SM that is
-// quicker than others take more of them (83.9 us against 85.2 at 230 units a run;
-// 38.9 against 37.4 at 56).
+// quicker than others take more of them (84.4 us against 85.6 at 230 units a run;
+// 60.8 against 59.4 at 120).
 constexpr int kLongRun = 100;
 struct Shares {
     int cluster, runs;
@@ -1262,7 +1264,7 @@ cudaError_t launch(const DecodeArgs &a, const Plan &p, cudaStream_t st, LaunchIn
     cudaError_t e;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     // CTAs fill one SM after another, so a grid that leaves room asks for as much shared memory as keeps it spread out
-    // (144 row tiles of 16 blocks in 288 CTAs: 8.9 us on 127 SMs, 7.9 us with two CTAs on each).
+    // (144 row tiles of 16 blocks in 288 CTAs: 8.4 us on 127 SMs, 7.9 us with two CTAs on each).
     const size_t smem_most = 227 * 1024;
     static std::atomic<unsigned long long> smem_set{0};
     if ((e = set_max_smem_once(reinterpret_cast<const void *>(decode_kernel<D, NT, Ctas>), smem_most, dev, smem_set)) !=

@@ -9,7 +9,8 @@
 // that agree so far; starting at the top bits, which scores of one size share,
 // every key would count in one bin).  Up to 256 keys are ranked by comparing each
 // with each instead, which has two barriers and not some twelve (choice and decode
-// over 128 blocks 11.0 -> 9.9 us, eviction of 16 blocks and reading 20.8 -> 18.5).
+// over 128 blocks 10.3 us against 11.3, eviction of 16 blocks and reading 17.7
+// against 20.1).
 //
 // The score of block J for query q is a bound on its keys' products with q,
 // with q in 8 bits too: c = rint(127 q / max|q|),

@@ -299,7 +299,7 @@ int attn_decode(const void *q, const void *k, const void *v, void *o, float *lse
  * p % 128: all of the open block and of the closed block before it.  So an
  * append of up to 64 tokens may be repeated, and tokens may be taken back
  * (drafted ones that were refused): lens may fall again as far as the start of
- * the last closed block.
+ * the block that was closed last when it was largest (since an eviction).
  *
  * The caller owns all of the memory (device; zeros at the start do).  Calls on
  * one cache are ordered by their stream; calls on different streams are the
@@ -379,10 +379,13 @@ size_t attn_q8_decode_workspace_bytes(const attn_q8_cache *cache, int H, int Tq,
  * cache's (query head h reads key head h / (H / cache H); at most 64 share
  * one).  1 <= Tq <= ATTN_DECODE_MAX_QUERIES.  Query r is the token at position
  * lens[b] - Tq + r; where that is below zero nothing is seen: o = 0, lse =
- * -inf.  workspace: at least attn_q8_decode_workspace_bytes bytes, 256-byte
- * aligned, its contents do not matter (NULL where that is 0).  One launch;
- * a second one joins the parts of few heads over many blocks, and another sums
- * the weights of those and of more than 16 rows (32 at D 32 and 64). */
+ * -inf.  Sums are float32 and not yet divided by the softmax's sum: values of
+ * 10^30 do not overflow over 10^5 tokens of one weight.  workspace: at least
+ * attn_q8_decode_workspace_bytes bytes, 256-byte aligned, its contents do not
+ * matter (NULL where that is 0).  One launch; a second one joins the parts of few
+ * heads over many blocks, and another sums the weights of those and of more than
+ * 16 rows (32 at D 32 and 64).  As the host does not know the lengths, that goes
+ * by the cache's capacity. */
 int attn_q8_decode(const attn_q8_cache *cache, const void *q, void *o, float *lse,
                    const int32_t *lens, int H, int Tq, float scale, const attn_strides *strides,
                    const attn_q8_decode_options *opts, void *workspace, size_t workspace_bytes,
@@ -409,10 +412,10 @@ size_t attn_q8_evict_workspace_bytes(const attn_q8_cache *cache);
 
 /* Drops closed blocks until each sequence and head has at most `keep` (>= 1) of
  * them: the first `sink` and the last `recent` ones stay, and of the others
- * those with the largest cache->weight (ties to the lowest index; sink +
- * recent <= keep).  The kept blocks move to the front in order, with scales,
- * bounds and weight, of `out`: the same cache (the same pointers), or another
- * one that shares no memory with it and holds at least min(keep, blocks)
+ * those with the largest cache->weight (ties to the lowest index, NaN first;
+ * sink + recent <= keep).  The kept blocks move to the front in order, with
+ * scales, bounds and weight, of `out`: the same cache (the same pointers), or
+ * another one that shares no memory with it and holds at least min(keep, blocks)
  * blocks.  lens_out [B] (lens, or apart from it) gets the new lengths:
  * min(closed, keep) * 64 + lens[b] % 64; kept int32 [B, H, keep] (apart from
  * both) the places the blocks came from, ascending, -1 behind the last.
