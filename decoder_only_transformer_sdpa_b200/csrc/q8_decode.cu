@@ -58,6 +58,7 @@ constexpr float kLn2 = 0.69314718055994531f;
 // eleven bits): 8, 3, 2 and 1 take 37.0, 33.9, 33.6 and 33.9 us over 16411 tokens of 4 x 8 heads of 128 with 16 rows,
 // whose scores spread by 1.8; without the light weights' check and products it were 31.8.
 constexpr float kPShift = 13.f, kSlack = 2.f, kLeastF16 = 0x1p-14f;
+constexpr float kUnit = 0x1p-13f;  // brings sums of P to those of exp2(s - m), whose logarithms are smaller and round less
 // Outputs are summed as 2^7 exp2(s - m) times the values (what P gives times kOutputs), so that values of 10^30 do not
 // overflow over 10^5 tokens of one weight; smaller sums would cost bits where a block's value scale is next to underflow
 // (10^-35 keeps 16 of them).
@@ -546,7 +547,7 @@ __device__ __forceinline__ void add(float4 &o, float f, const float4 &o1) {
 }
 
 // log2 of a row's sum, in the units of the blocks' sums; a row that sees nothing gives nothing.
-__device__ __forceinline__ float row_total(float m, float l) { return l == 0.f ? INFINITY : m + lg2(l); }
+__device__ __forceinline__ float row_total(float m, float l) { return l == 0.f ? INFINITY : m + lg2(l * kUnit); }
 
 // Row `r` of a group: where its output goes, and its lse.
 __device__ __forceinline__ long long row_place(const DecodeArgs &a, const Where &w, int r) {
@@ -555,7 +556,7 @@ __device__ __forceinline__ long long row_place(const DecodeArgs &a, const Where 
 }
 __device__ __forceinline__ void write_lse(const DecodeArgs &a, const Where &w, int r, float m, float l) {
     a.lse[((long long)w.b * a.H + w.h * a.G + row_head(a, r)) * a.Tq + row_token(a, w, r)] =
-        l == 0.f ? -INFINITY : (m + (log2f(l) - kPShift)) * kLn2;
+        l == 0.f ? -INFINITY : (m + log2f(l * kUnit)) * kLn2;
     if (a.part.total) a.part.total[w.bh * (a.tiles * a.tile_rows) + r] = row_total(m, l);
 }
 // What a row's sums are multiplied by; nothing seen: zeros.
@@ -917,7 +918,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, Ctas>::kCtas) decode_kern
                         const int row = w.tile * kRows + nt * 8 + 2 * t + x;
                         if (g == 0 && row < a.rows)
                             a.part.lb[(w.bh * a.c.blocks + id) * a.rows + row] =
-                                v == 0.f ? -INFINITY : st.m[nt][x] + lg2(v);
+                                v == 0.f ? -INFINITY : st.m[nt][x] + lg2(v * kUnit);
                     }
             }
             const float vscale = sc.y * kOutputs;

@@ -126,6 +126,20 @@ def test_decode_values_near_the_ends_of_float32(D, size, n, room):
         assert abs(float(lse[0, h, 0]) - el) <= tl
 
 
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_lse_of_equal_scores(D):
+    """n scores of zero: lse = log n. Rounded are log2 (one unit of its result, 2^-23 of it at most), the product with
+    ln 2 and ln 2 itself (2^-24 and 2^-25), and the sum of exp2's (2^-22 each, and so of the sum)."""
+    lens = [*range(1, 40), 63, 64, 65, 100, 127, 128, 500, 777, 1000, 3000]
+    c = A.Q8Cache.empty(len(lens), 1, D, max(lens), device=dev())
+    o, lse = A.attn_q8_decode(torch.zeros(len(lens), 1, 1, D, dtype=torch.bfloat16, device=dev()), c,
+                              torch.tensor(lens, dtype=torch.int32, device=dev()))
+    assert status() == 0 and (o == 0).all()
+    want = np.log(np.array(lens, np.float64))
+    err = np.abs(lse[:, 0, 0].double().cpu().numpy() - want)
+    assert np.all(err <= 2.0**-22 * (1 + want)), list(zip(lens, err / (2.0**-22 * (1 + want))))
+
+
 # ------------------------------------------------------ lists out of order
 
 
